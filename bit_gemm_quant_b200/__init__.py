@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from collections import namedtuple
 
 SYM, ASYM = 0, 1
 # OR-ed into the mode of w4a16_gemm / w4a16_gemm_noalloc: the packed weight is
@@ -24,6 +25,7 @@ REPACKED = 0x400
 NVFP4, MXFP4 = 0, 1
 FP4_BLOCK = {NVFP4: 16, MXFP4: 32}
 MX_SCALES_ROWS, MX_SCALES_MMA = 0, 1
+SOFTMAX, SIGMOID = 0, 1
 W4_OK, W4_ERR_INVALID_ARG, W4_ERR_UNSUPPORTED, W4_ERR_CUDA = 0, 1, 2, 3
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libw4.so")
@@ -74,6 +76,15 @@ def lib() -> ctypes.CDLL:
         L.w4_mx_scale_layout.restype = I
         L.w4_mx_gemm.argtypes = [P, P, I64, I64, I64, P, P, P, I, P]
         L.w4_mx_gemm.restype = I
+        F = ctypes.c_float
+        L.w4_rmsnorm.argtypes = [P, P, P, I64, I64, F, P, P, P, P, I, P]
+        L.w4_rmsnorm.restype = I
+        L.w4_route.argtypes = [P, I, P, I64, I, I, I, I, I, I, I, F, P, P, P, P, P, P]
+        L.w4_route.restype = I
+        L.w4a16_experts_gemm.argtypes = [P, I64, P, P, I, I, I64, I64, I64, P, P, P, I, I, P, P]
+        L.w4a16_experts_gemm.restype = I
+        L.w4_combine.argtypes = [P, I64, P, P, I64, I, I64, P, P, P]
+        L.w4_combine.restype = I
         L.w4_status_string.argtypes = [I]
         L.w4_status_string.restype = ctypes.c_char_p
         L.w4_layout_version.argtypes = []
@@ -151,6 +162,26 @@ def w4_mx_scale_layout(src, R, K, dst, stream) -> int:
 
 def w4_mx_gemm(x_codes, x_scales, M, N, K, w_codes, w_scales, Y, flags, stream) -> int:
     return lib().w4_mx_gemm(x_codes, x_scales, M, N, K, w_codes, w_scales, Y, flags, stream)
+
+
+def w4_rmsnorm(X, residual, gamma, M, K, eps, H, Y, codes, scales, scale_layout, stream) -> int:
+    return lib().w4_rmsnorm(X, residual, gamma, M, K, eps, H, Y, codes, scales, scale_layout, stream)
+
+
+def w4_route(logits, logits_type, bias, T, E, top_k, scoring, n_groups, topk_groups, group_top, renormalize, scale,
+             ids, weights, offsets, order, pos, stream) -> int:
+    return lib().w4_route(logits, logits_type, bias, T, E, top_k, scoring, n_groups, topk_groups, group_top,
+                          renormalize, scale, ids, weights, offsets, order, pos, stream)
+
+
+def w4a16_experts_gemm(X, R, offsets, order, top_k, E, P, N, K, qweight, scales, qzeros, group, mode, Y,
+                       stream) -> int:
+    return lib().w4a16_experts_gemm(X, R, offsets, order, top_k, E, P, N, K, qweight, scales, qzeros, group, mode, Y,
+                                    stream)
+
+
+def w4_combine(Y, P, pos, weights, T, top_k, N, add, out, stream) -> int:
+    return lib().w4_combine(Y, P, pos, weights, T, top_k, N, add, out, stream)
 
 
 def w4_status_string(status: int) -> str:
@@ -391,3 +422,182 @@ def mx_gemm(x_codes, x_scales, w_codes, w_scales, out=None, stream=None, weights
     if st != W4_OK:
         raise W4Error(st, "w4_mx_gemm")
     return Y
+
+
+# --- the operators around a layer of experts -----------------------------------
+#
+# These helpers check what the C entry points cannot see (types, shapes,
+# contiguity, one device), and run on the tensors' device, on its current
+# stream unless ``stream`` is given.
+
+def _need(t, what: str, dtype, shape, like=None):
+    """ValueError unless t is a contiguous CUDA tensor of this dtype and shape, on like's device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s: a contiguous %s tensor of shape %s is needed, got %s %s"
+                         % (what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    if like is None:
+        if not t.is_cuda:
+            raise ValueError("%s: a CUDA tensor is needed" % what)
+    elif t.device != like.device:
+        raise ValueError("%s is on %s, not on %s" % (what, t.device, like.device))
+
+
+def _run(name: str, entry, device, stream, *args):
+    """entry(*args, stream) with the tensors' device current; W4Error on a nonzero status."""
+    import torch
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _run(name, entry, device, stream, *args)
+    handle = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    st = entry(*args, handle)
+    if st != W4_OK:
+        raise W4Error(st, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_checks(X, gamma, residual):
+    import torch
+    if X.dim() != 2:
+        raise ValueError("X: a tensor of shape [M, K] is needed")
+    _need(X, "X", torch.bfloat16, X.shape)
+    _need(gamma, "gamma", torch.bfloat16, X.shape[1:], X)
+    if residual is not None:
+        _need(residual, "residual", torch.bfloat16, X.shape, X)
+
+
+def rmsnorm(X, gamma, eps: float, residual=None, out=None, stream=None):
+    """RMS norm of the rows of X[M,K] (bf16 CUDA): returns (Y, H) in bf16 with
+    h = X + residual, Y = h / sqrt(mean h^2 + eps) * gamma and H = h; H is None
+    without a residual.  ``out`` = (Y, H): Y may be X, H may be X or the
+    residual."""
+    import torch
+    _norm_checks(X, gamma, residual)
+    if out is None:
+        Y, H = torch.empty_like(X), None if residual is None else torch.empty_like(X)
+    else:
+        Y, H = out
+        _need(Y, "out[0]", torch.bfloat16, X.shape, X)
+        if H is not None:
+            _need(H, "out[1]", torch.bfloat16, X.shape, X)
+    _run("w4_rmsnorm", lib().w4_rmsnorm, X.device, stream, X.data_ptr(), _addr(residual), gamma.data_ptr(),
+         X.shape[0], X.shape[1], eps, _addr(H), Y.data_ptr(), None, None, MX_SCALES_ROWS)
+    return Y, H
+
+
+def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SCALES_MMA, out=None, stream=None):
+    """``rmsnorm`` quantized to MXFP8 in the same pass: returns (codes uint8
+    [M, K], scales uint8 in ``scale_layout`` as ``mxfp8_quant`` gives them, H).
+    ``out`` = (codes, scales, H)."""
+    import torch
+    _norm_checks(X, gamma, residual)
+    M, K = X.shape
+    rows = scale_layout == MX_SCALES_ROWS
+    if out is None:
+        codes = torch.empty((M, K), dtype=torch.uint8, device=X.device)
+        scales = torch.empty((M, max(K // 32, 1)) if rows else (max(mx_scale_bytes(M, K), 1),), dtype=torch.uint8,
+                             device=X.device)
+        H = None if residual is None else torch.empty_like(X)
+    else:
+        codes, scales, H = out
+        _need(codes, "out[0]", torch.uint8, X.shape, X)
+        _need(scales, "out[1]", torch.uint8, (M, K // 32) if rows else (mx_scale_bytes(M, K),), X)
+        if H is not None:
+            _need(H, "out[2]", torch.bfloat16, X.shape, X)
+    _run("w4_rmsnorm", lib().w4_rmsnorm, X.device, stream, X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps,
+         _addr(H), None, codes.data_ptr(), scales.data_ptr(), scale_layout)
+    return codes, scales, H
+
+
+Routing = namedtuple("Routing", "ids weights offsets order pos")
+
+
+def route(logits, top_k: int, scoring: int = SOFTMAX, bias=None, n_groups: int = 1, topk_groups: int = 1,
+          group_top: int = 1, renormalize: bool = True, scale: float = 1.0, out=None, stream=None):
+    """Routing of the tokens behind logits[T,E] (fp32 or bf16 CUDA) to top_k of
+    E experts: a ``Routing`` of ids int32 [T, top_k], weights fp32 [T, top_k] and
+    the plan of the experts' rows: offsets int32 [E + 1], order int32
+    [T * top_k], pos int32 [T, top_k] (what ``experts_gemm`` and ``combine``
+    read).  ``bias`` (fp32 [E]) is added to the scores for the choice alone.
+    Masked experts (logit -inf) are never chosen: id -1 where none is left."""
+    import torch
+    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("logits: an fp32 or bf16 tensor of shape [T, E] is needed")
+    _need(logits, "logits", logits.dtype, logits.shape)
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,), logits)
+    if out is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=logits.device)
+        order = torch.empty(T * top_k, dtype=torch.int32, device=logits.device)
+        pos = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    else:
+        ids, weights, offsets, order, pos = out
+        for t, what, dtype, shape in ((ids, "ids", torch.int32, (T, top_k)), (weights, "weights", torch.float32, (T, top_k)),
+                                      (offsets, "offsets", torch.int32, (E + 1,)), (order, "order", torch.int32, (T * top_k,)),
+                                      (pos, "pos", torch.int32, (T, top_k))):
+            _need(t, what, dtype, shape, logits)
+    _run("w4_route", lib().w4_route, logits.device, stream, logits.data_ptr(), 1 if logits.dtype is torch.float32 else 0,
+         _addr(bias), T, E, top_k, scoring, n_groups, topk_groups, group_top, 1 if renormalize else 0, scale,
+         ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), pos.data_ptr())
+    return Routing(ids, weights, offsets, order, pos)
+
+
+def experts_gemm(X, qweight, scales, qzeros, group: int, mode: int, offsets, order=None, top_k: int = 1, out=None,
+                 stream=None):
+    """The W4A16 product by expert: Y[i] = X[row] . W[e]^T for the sorted rows
+    offsets[e] <= i < offsets[e + 1] of a ``route`` plan, row = order[i] // top_k
+    (i itself without ``order``: X holds the sorted rows already).  qweight int32
+    [E, N, K/8], scales fp16 [E, N, K/group] and qzeros int32 [E, N,
+    ceil(K/group/8)] (None in SYM mode) are ``quant_pack``'s, stacked.  Returns
+    Y bf16 [order.numel() or X.shape[0], N]; rows from offsets[E] on are not
+    written."""
+    import torch
+    if X.dim() != 2 or qweight.dim() != 3 or group < 1:
+        raise ValueError("X [R, K], qweight [E, N, K/8] and a group size are needed")
+    R, K = X.shape
+    E, N = qweight.shape[:2]
+    _need(X, "X", torch.bfloat16, X.shape)
+    _need(qweight, "qweight", torch.int32, (E, N, K // 8), X)
+    _need(scales, "scales", torch.float16, (E, N, K // group), X)
+    if qzeros is not None:
+        _need(qzeros, "qzeros", torch.int32, (E, N, (K // group + 7) // 8), X)
+    _need(offsets, "offsets", torch.int32, (E + 1,), X)
+    P = R
+    if order is not None:
+        P = order.numel()
+        _need(order, "order", torch.int32, (P,), X)
+    if out is None:
+        out = torch.empty((P, N), dtype=torch.bfloat16, device=X.device)
+    else:
+        _need(out, "out", torch.bfloat16, (P, N), X)
+    _run("w4a16_experts_gemm", lib().w4a16_experts_gemm, X.device, stream, X.data_ptr(), R, offsets.data_ptr(),
+         _addr(order), top_k, E, P, N, K, qweight.data_ptr(), scales.data_ptr(), _addr(qzeros), group, mode,
+         out.data_ptr())
+    return out
+
+
+def combine(Y, pos, weights, add=None, out=None, stream=None):
+    """out[t] = add[t] + sum_j weights[t, j] * Y[pos[t, j]] (bf16 [T, N]) from an
+    ``experts_gemm`` result Y[P, N] and a ``route`` plan's pos and weights
+    [T, top_k]; positions of -1 add nothing.  ``out`` may be ``add``."""
+    import torch
+    if Y.dim() != 2 or pos.dim() != 2:
+        raise ValueError("Y [P, N] and pos [T, top_k] are needed")
+    (P, N), (T, top_k) = Y.shape, pos.shape
+    _need(Y, "Y", torch.bfloat16, Y.shape)
+    _need(pos, "pos", torch.int32, pos.shape, Y)
+    _need(weights, "weights", torch.float32, pos.shape, Y)
+    if add is not None:
+        _need(add, "add", torch.bfloat16, (T, N), Y)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.bfloat16, device=Y.device)
+    else:
+        _need(out, "out", torch.bfloat16, (T, N), Y)
+    _run("w4_combine", lib().w4_combine, Y.device, stream, Y.data_ptr(), P, pos.data_ptr(), weights.data_ptr(), T,
+         top_k, N, _addr(add), out.data_ptr())
+    return out

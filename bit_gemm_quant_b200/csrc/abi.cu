@@ -1,7 +1,9 @@
 // extern "C" entry points of libw4 (declared in include/w4.h): argument
 // validation on the host, then dispatch to the kernels.  Nothing here
 // allocates device memory or synchronizes a stream.
-#include "common.cuh"
+#include "experts.cuh"
+
+#include <math.h>
 
 namespace {
 
@@ -243,6 +245,81 @@ w4_status w4_awq_search(const void *W, const void *X, int64_t N, int64_t K, int6
         return W4_ERR_UNSUPPORTED;
     const cudaError_t e = w4::launch_awq_search(W, X, N, K, M, group, mode, n_alpha, losses, best, s_best,
                                                 workspace, (cudaStream_t)stream);
+    return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+w4_status w4_rmsnorm(const void *X, const void *residual, const void *gamma, int64_t M, int64_t K, float eps,
+                     void *H, void *Y, uint8_t *codes, uint8_t *scales, int scale_layout, w4_stream_t stream)
+{
+    if (!X || !gamma || (!Y && !codes) || (codes != nullptr) != (scales != nullptr)) return W4_ERR_INVALID_ARG;
+    if (H && !residual) return W4_ERR_INVALID_ARG;
+    if (scale_layout != W4_MX_SCALES_ROWS && scale_layout != W4_MX_SCALES_MMA) return W4_ERR_INVALID_ARG;
+    if (M < 1 || K < 1 || !fits(w4::mx_padded_rows(M), K) || !(eps > 0.f) || isinf(eps)) return W4_ERR_INVALID_ARG;
+    const size_t align = codes ? 16 : 2;
+    if (!aligned(X, align) || !aligned(residual, align) || !aligned(gamma, align) || !aligned(H, align) ||
+        !aligned(Y, align))
+        return W4_ERR_INVALID_ARG;
+    if (codes) {
+        const bool mma = scale_layout == W4_MX_SCALES_MMA;
+        if (K % (mma ? 128 : 32) != 0 || !aligned(codes, 16) || (mma && !aligned(scales, 16))) return W4_ERR_INVALID_ARG;
+    }
+    if (K > 32768 || M > INT32_MAX - 128) return W4_ERR_UNSUPPORTED;
+    const cudaError_t e = w4::launch_rmsnorm(X, residual, gamma, M, K, eps, H, Y, codes, scales, scale_layout,
+                                             (cudaStream_t)stream);
+    return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+w4_status w4_route(const void *logits, int logits_type, const float *bias, int64_t T, int E, int top_k, int scoring,
+                   int n_groups, int topk_groups, int group_top, int renormalize, float scale, int32_t *ids,
+                   float *weights, int32_t *offsets, int32_t *order, int32_t *pos, w4_stream_t stream)
+{
+    if (!logits || !ids || !weights) return W4_ERR_INVALID_ARG;
+    if ((offsets != nullptr) != (order != nullptr) || (offsets != nullptr) != (pos != nullptr)) return W4_ERR_INVALID_ARG;
+    if (logits_type != W4_LOGITS_BF16 && logits_type != W4_LOGITS_F32) return W4_ERR_INVALID_ARG;
+    if (scoring != W4_SOFTMAX && scoring != W4_SIGMOID) return W4_ERR_INVALID_ARG;
+    if (T < 1 || E < 1 || E > 1024 || top_k < 1 || top_k > 32) return W4_ERR_INVALID_ARG;
+    if (n_groups < 1 || n_groups > 64 || E % n_groups != 0 || topk_groups < 1 || topk_groups > n_groups ||
+        (group_top != 1 && group_top != 2) || top_k > topk_groups * (E / n_groups) || !isfinite(scale))
+        return W4_ERR_INVALID_ARG;
+    if (!aligned(logits, logits_type == W4_LOGITS_F32 ? 4 : 2) || !aligned(bias, 4) || !aligned(ids, 4) ||
+        !aligned(weights, 4) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(pos, 4))
+        return W4_ERR_INVALID_ARG;
+    if (T > (1 << 30) / E || T > (1 << 30) / top_k) return W4_ERR_UNSUPPORTED;
+    const cudaError_t e = w4::launch_route(logits, logits_type == W4_LOGITS_F32, bias, T, E, top_k,
+                                           scoring == W4_SIGMOID, n_groups, topk_groups, group_top, renormalize != 0,
+                                           scale, ids, weights, offsets, order, pos, (cudaStream_t)stream);
+    return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+w4_status w4a16_experts_gemm(const void *X, int64_t R, const int32_t *offsets, const int32_t *order, int top_k, int E,
+                             int64_t P, int64_t N, int64_t K, const uint32_t *qweight, const void *scales,
+                             const uint32_t *qzeros, int group, int mode, void *Y, w4_stream_t stream)
+{
+    if (!X || !offsets || !qweight || !scales || !Y) return W4_ERR_INVALID_ARG;
+    if (!group_ok(group) || !mode_ok(mode)) return W4_ERR_INVALID_ARG;
+    if (E < 1 || E > 1024 || P < 1 || R < 1 || (order && top_k < 1) || (!order && R < P)) return W4_ERR_INVALID_ARG;
+    if (N < 1 || K < group || K % group != 0 || !fits(N, E) || !fits(N * E, K) || !fits(R, K) || !fits(P, N))
+        return W4_ERR_INVALID_ARG;
+    if ((mode == W4_ASYM) != (qzeros != nullptr)) return W4_ERR_INVALID_ARG;
+    if (!aligned(X, 16) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(qweight, 16) || !aligned(scales, 2) ||
+        !aligned(qzeros, 4) || !aligned(Y, 2))
+        return W4_ERR_INVALID_ARG;
+    if (N * E > INT32_MAX - 256 || P > (1 << 30) || R > INT32_MAX || K > INT32_MAX) return W4_ERR_UNSUPPORTED;
+    const w4::ExpertPlan plan = {offsets, order, order ? top_k : 1, E, (int)R, (int)P};
+    if (w4::max_units(P, E, 8) > 65535) return W4_ERR_UNSUPPORTED;
+    const cudaError_t e =
+        w4::launch_experts_gemv(X, plan, N, K, qweight, scales, qzeros, group, mode, Y, (cudaStream_t)stream);
+    return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
+}
+
+w4_status w4_combine(const void *Y, int64_t P, const int32_t *pos, const float *weights, int64_t T, int top_k,
+                     int64_t N, const void *add, void *out, w4_stream_t stream)
+{
+    if (!Y || !pos || !weights || !out) return W4_ERR_INVALID_ARG;
+    if (P < 1 || T < 1 || N < 1 || top_k < 1 || top_k > 32 || !fits(P, N) || !fits(T, N)) return W4_ERR_INVALID_ARG;
+    if (!aligned(Y, 2) || !aligned(pos, 4) || !aligned(weights, 4) || !aligned(add, 2) || !aligned(out, 2))
+        return W4_ERR_INVALID_ARG;
+    const cudaError_t e = w4::launch_combine(Y, P, pos, weights, T, top_k, N, add, out, (cudaStream_t)stream);
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 

@@ -123,6 +123,18 @@ cudaError_t launch_gemm_tc(const void *X, int64_t M, int64_t N, int64_t K, const
 size_t awq_workspace_bytes(int64_t M, int64_t N, int64_t K, int group, int mode, int n_alpha);
 cudaError_t launch_awq_search(const void *W, const void *X, int64_t N, int64_t K, int64_t M, int group, int mode,
                               int n_alpha, double *losses, int *best, float *s_best, void *ws, cudaStream_t stream);
+cudaError_t launch_rmsnorm(const void *X, const void *residual, const void *gamma, int64_t M, int64_t K, float eps,
+                           void *H, void *Y, uint8_t *codes, uint8_t *scales, int layout, cudaStream_t stream);
+// routing, the products by expert (the plan: experts.cuh) and the sum over a token's experts
+cudaError_t launch_route(const void *logits, int f32, const float *bias, int64_t T, int E, int k, int sigmoid,
+                         int groups, int keep, int group_top, int renorm, float scale, int *ids, float *weights,
+                         int *offsets, int *order, int *pos, cudaStream_t stream);
+struct ExpertPlan;
+cudaError_t launch_experts_gemv(const void *X, const ExpertPlan &plan, int64_t N, int64_t K, const uint32_t *qweight,
+                                const void *scales, const uint32_t *qzeros, int group, int mode, void *Y,
+                                cudaStream_t stream);
+cudaError_t launch_combine(const void *Y, int64_t P, const int *pos, const float *weights, int64_t T, int k, int64_t N,
+                           const void *add, void *out, cudaStream_t stream);
 int read_and_clear_device_error();
 // Time after which a kernel's wait for a copy, an MMA or another warp gives up
 // (default kDefaultWaitNs; lowered only by tests of the failure path through

@@ -20,21 +20,12 @@
 // that the IEEE division would also make (2^-e is a normal fp32 power of two
 // for every e in range), followed by the hardware's saturating round-to-
 // nearest-even E4M3 conversion.
-#include "common.cuh"
+#include "mx_layout.cuh"
 
 #include <cuda_fp8.h>
 
 namespace w4 {
 namespace {
-
-// Byte offset of the scale of (row r, 32-element block kb) in the tensor-core
-// layout of a matrix with K columns: 512-byte atoms of 128 rows x 4 blocks,
-// row r of an atom at 16 * (r % 32) + 4 * (r / 32), block kb % 4 in the byte
-// of that 32-bit word; atoms ordered by k within a 128-row band.
-__host__ __device__ __forceinline__ int64_t mma_sf_offset(int64_t r, int64_t kb, int64_t K)
-{
-    return (((r >> 7) * (K >> 7) + (kb >> 2)) << 9) + ((r & 31) << 4) + (((r >> 5) & 3) << 2) + (kb & 3);
-}
 
 template <int LAYOUT>
 __global__ void __launch_bounds__(256) mxfp8_quant_kernel(const uint4 *__restrict__ X, int64_t M, int64_t rows,

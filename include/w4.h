@@ -399,6 +399,145 @@ w4_status w4_mx_scale_layout(const uint8_t *src, int64_t R, int64_t K, uint8_t *
 w4_status w4_mx_gemm(const uint8_t *x_codes, const uint8_t *x_scales, int64_t M, int64_t N, int64_t K,
                      const uint8_t *w_codes, const uint8_t *w_scales, void *Y, int flags, w4_stream_t stream);
 
+/*
+ * w4_rmsnorm -- root-mean-square norm of bf16 rows, with the residual's
+ * addition in front of it and, behind it, the quantization that w4_mx_gemm's
+ * activations need.
+ *   Exact semantics, for each row of K elements (fp32 unless stated):
+ *     h    = x + r                       (h = x when residual == NULL)
+ *     H    = bf16_rne(h)                 (stored only; the norm goes on from h)
+ *     y    = (h / sqrt(mean h^2 + eps)) * gamma
+ *     Y    = bf16_rne(y)
+ *     codes, scales: w4_mxfp8_quant's rule on y itself (y is not rounded to
+ *     bf16 first): per 32 elements e = clamp(floor(log2 amax|y|) - 8, -127, 127),
+ *     scale code e + 127, code = e4m3_rne_satfinite(y / 2^e)
+ *   A row's sum of squares must not overflow fp32.
+ *   X        bf16 [M][K].
+ *   residual bf16 [M][K], or NULL.
+ *   gamma    bf16 [K].
+ *   M, K     M >= 1, 1 <= K <= 32768; with codes K % 32 == 0, and K % 128 == 0
+ *            for W4_MX_SCALES_MMA.  X, residual, gamma, H and Y need 2-byte
+ *            alignment (16 bytes for all of them and K % 8 == 0 run faster).
+ *   eps      finite, > 0.
+ *   H        out, bf16 [M][K], or NULL; needs a residual.  May be the residual
+ *            or X itself.
+ *   Y        out, bf16 [M][K], or NULL; may be X itself.
+ *   codes    out, uint8 [M][K] E4M3 codes, 16-byte aligned, or NULL.
+ *   scales   out, E8M0 codes in `scale_layout`, as w4_mxfp8_quant writes them
+ *            (W4_MX_SCALES_MMA: 16-byte aligned, padding rows 0); NULL exactly
+ *            when codes is.
+ *   At least one of Y and codes; both may be asked for at once.  With codes
+ *   every bf16 pointer must be 16-byte aligned.
+ * Other overlaps of outputs with inputs are not allowed.  Errors:
+ * W4_ERR_INVALID_ARG for a NULL or misaligned pointer, a bad size, eps or
+ * layout; W4_ERR_UNSUPPORTED for K > 32768; W4_ERR_CUDA if the launch fails.
+ * Asynchronous on `stream`.
+ */
+w4_status w4_rmsnorm(const void *X, const void *residual, const void *gamma, int64_t M, int64_t K, float eps,
+                     void *H, void *Y, uint8_t *codes, uint8_t *scales, int scale_layout, w4_stream_t stream);
+
+/* Types of the router's logits, and its scoring functions. */
+typedef enum { W4_LOGITS_BF16 = 0, W4_LOGITS_F32 = 1 } w4_logits_type;
+typedef enum { W4_SOFTMAX = 0, W4_SIGMOID = 1 } w4_scoring;
+
+/*
+ * w4_route -- routing of T tokens to top_k of E experts, and the plan that
+ * w4a16_experts_gemm and w4_combine read.
+ *   Exact semantics, for each token (scores in fp64):
+ *     score[e]  = softmax over the E logits, or sigmoid(logit)
+ *     choice[e] = score[e] + bias[e]        (the bias steers the choice only)
+ *     groups    : the E experts are n_groups runs of E / n_groups; a group's
+ *                 value is the sum of its group_top largest choices; only the
+ *                 topk_groups best groups stay
+ *     chosen    : the top_k largest choices among them, largest first; equal
+ *                 choices (and equal groups) go to the lowest index
+ *     weight    = score of the chosen expert, divided by the sum of the chosen
+ *                 scores when renormalize != 0, times scale; rounded to fp32
+ *   A logit of -infinity masks its expert for that token: score 0, never
+ *   chosen, nothing added to its group's value (a group with no other expert
+ *   is never kept before one that has).  Where fewer than top_k experts can be
+ *   chosen the rest have id -1, weight 0 and position -1; a token whose logits
+ *   are all -infinity (padding) gets no expert at all.  A NaN or +infinity
+ *   among a token's logits gives unspecified choices and weights for that
+ *   token, with ids that stay -1 or distinct and below E.  Scores that differ by less
+ *   than fp64 resolves count as equal or not, whichever way they round.
+ *   The plan: the pairs p = t * top_k + j with an expert, sorted by expert and,
+ *   for one expert, by p.
+ *   logits   bf16 or fp32 [T][E], by `logits_type`; 2- or 4-byte aligned.
+ *   bias     fp32 [E], finite, or NULL.
+ *   T, E     T >= 1, 1 <= E <= 1024.
+ *   top_k    1..32, at most topk_groups * (E / n_groups).
+ *   n_groups, topk_groups: E % n_groups == 0, n_groups <= 64,
+ *            1 <= topk_groups <= n_groups (1 and 1: no groups).
+ *   group_top 1 or 2 (1 with a group of one expert means the same).
+ *   scale    finite.
+ *   ids      out, int32 [T][top_k].
+ *   weights  out, fp32 [T][top_k].
+ *   offsets  out, int32 [E + 1]: the sorted pairs of expert e are rows
+ *            offsets[e] .. offsets[e + 1] - 1; offsets[0] = 0.
+ *   order    out, int32 [T * top_k]: the pair of each sorted row; -1 behind
+ *            the last, offsets[E].
+ *   pos      out, int32 [T][top_k]: the sorted row of each pair, or -1.
+ * offsets, order and pos are all given or all NULL (then only the choice is
+ * made).  All outputs 4-byte aligned, every element is written.  Errors:
+ * W4_ERR_INVALID_ARG for a NULL or misaligned pointer or a bad size or option;
+ * W4_ERR_UNSUPPORTED for T * top_k or T * E above 2^30; W4_ERR_CUDA if a
+ * launch fails.  Asynchronous on `stream`; results repeat bit for bit.
+ */
+w4_status w4_route(const void *logits, int logits_type, const float *bias, int64_t T, int E, int top_k, int scoring,
+                   int n_groups, int topk_groups, int group_top, int renormalize, float scale, int32_t *ids,
+                   float *weights, int32_t *offsets, int32_t *order, int32_t *pos, w4_stream_t stream);
+
+/*
+ * w4a16_experts_gemm -- w4a16_gemm for the rows of many experts at once:
+ *   Y[i] = X[row(i)] . W^[e(i)]^T     for i < offsets[E], offsets[e] <= i < offsets[e + 1],
+ * with row(i) = order[i] / top_k, or i when order is NULL, and W^ dequantized
+ * and Y rounded as in w4a16_gemm.
+ *   X        bf16 [R][K], 16-byte aligned: the tokens when order is given
+ *            (the experts' first product), the sorted rows when it is NULL (a
+ *            product of such a product's output).
+ *   R        rows of X, R >= 1 (R >= P when order is NULL).
+ *   offsets  int32 [E + 1] device array, as w4_route writes it.
+ *   order    int32 [P] device array (w4_route's), or NULL.
+ *   top_k    >= 1; ignored when order is NULL.
+ *   E        1..1024 experts.
+ *   P        rows of Y, >= 1: the most that offsets[E] can be (T * top_k).
+ *   N, K     N >= 1, K % group == 0, K >= group.
+ *   qweight, scales, qzeros: w4_quant_pack's arrays of the E weights [N][K],
+ *            one expert after the other: uint32 [E][N][K/8], fp16 [E][N][K/g],
+ *            uint32 [E][N][ceil(K/g/8)] (NULL in W4_SYM mode).
+ *   mode     W4_SYM or W4_ASYM; no flags.
+ *   Y        out, bf16 [P][N], 2-byte aligned.  The rows from offsets[E] on
+ *            are left as they were.
+ * The plan stays on the device: nothing of the call depends on the host
+ * knowing it, so the call can be captured and replayed with other plans of the
+ * same P.  Values of offsets outside [0, P] are taken as the nearest of the
+ * two and rows outside [0, R) as its ends, so a wrong plan gives wrong rows of
+ * Y, never an access outside the arrays.  Errors as for w4a16_gemm;
+ * W4_ERR_UNSUPPORTED for shapes past 32-bit indexing (E * N, P, R, K, and the
+ * number of tiles).  Needs no workspace.  Asynchronous on `stream`; results
+ * repeat bit for bit.
+ */
+w4_status w4a16_experts_gemm(const void *X, int64_t R, const int32_t *offsets, const int32_t *order, int top_k, int E,
+                             int64_t P, int64_t N, int64_t K, const uint32_t *qweight, const void *scales,
+                             const uint32_t *qzeros, int group, int mode, void *Y, w4_stream_t stream);
+
+/*
+ * w4_combine -- the weighted sum over each token's experts:
+ *   out[t] = bf16_rne(add[t] + sum_j weights[t][j] * Y[pos[t][j]]), in fp32, j in
+ * order; pairs whose position is outside [0, P) (w4_route's -1) add nothing.
+ *   Y        bf16 [P][N] (w4a16_experts_gemm's), 2-byte aligned.
+ *   pos, weights: int32 and fp32 [T][top_k], as w4_route writes them.
+ *   P, T, N  >= 1;  top_k 1..32.
+ *   add      bf16 [T][N] (a shared expert's output, or the residual), or NULL.
+ *   out      out, bf16 [T][N]; may be `add` itself, otherwise must not overlap
+ *            an input.  (Rows of 16-byte aligned vectors, N % 8 == 0, run faster.)
+ * Errors: W4_ERR_INVALID_ARG for a NULL or misaligned pointer or a bad size;
+ * W4_ERR_CUDA if the launch fails.  Asynchronous on `stream`.
+ */
+w4_status w4_combine(const void *Y, int64_t P, const int32_t *pos, const float *weights, int64_t T, int top_k,
+                     int64_t N, const void *add, void *out, w4_stream_t stream);
+
 /* Text for a status code; never NULL. */
 const char *w4_status_string(int status);
 
