@@ -11,6 +11,7 @@ missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from collections import namedtuple
 
@@ -81,7 +82,9 @@ def lib() -> ctypes.CDLL:
         L.w4_rmsnorm.restype = I
         L.w4_route.argtypes = [P, I, P, I64, I, I, I, I, I, I, I, F, P, P, P, P, P, P]
         L.w4_route.restype = I
-        L.w4a16_experts_gemm.argtypes = [P, I64, P, P, I, I, I64, I64, I64, P, P, P, I, I, P, P]
+        L.w4a16_experts_workspace_bytes.argtypes = [I64, I, I64, I]
+        L.w4a16_experts_workspace_bytes.restype = SZ
+        L.w4a16_experts_gemm.argtypes = [P, I64, P, P, I, I, I64, I64, I64, P, P, P, I, I, P, P, SZ, P]
         L.w4a16_experts_gemm.restype = I
         L.w4_combine.argtypes = [P, I64, P, P, I64, I, I64, P, P, P]
         L.w4_combine.restype = I
@@ -174,10 +177,14 @@ def w4_route(logits, logits_type, bias, T, E, top_k, scoring, n_groups, topk_gro
                           renormalize, scale, ids, weights, offsets, order, pos, stream)
 
 
-def w4a16_experts_gemm(X, R, offsets, order, top_k, E, P, N, K, qweight, scales, qzeros, group, mode, Y,
-                       stream) -> int:
+def w4a16_experts_workspace_bytes(P, E, K, gathered) -> int:
+    return int(lib().w4a16_experts_workspace_bytes(P, E, K, gathered))
+
+
+def w4a16_experts_gemm(X, R, offsets, order, top_k, E, P, N, K, qweight, scales, qzeros, group, mode, Y, workspace,
+                       workspace_bytes, stream) -> int:
     return lib().w4a16_experts_gemm(X, R, offsets, order, top_k, E, P, N, K, qweight, scales, qzeros, group, mode, Y,
-                                    stream)
+                                    workspace, workspace_bytes, stream)
 
 
 def w4_combine(Y, P, pos, weights, T, top_k, N, add, out, stream) -> int:
@@ -428,7 +435,7 @@ def mx_gemm(x_codes, x_scales, w_codes, w_scales, out=None, stream=None, weights
 #
 # These helpers check what the C entry points cannot see (types, shapes,
 # contiguity, one device), and run on the tensors' device, on its current
-# stream unless ``stream`` is given.
+# stream unless a ``stream=`` is given.
 
 def _need(t, what: str, dtype, shape, like=None):
     """ValueError unless t is a contiguous CUDA tensor of this dtype and shape, on like's device."""
@@ -442,14 +449,29 @@ def _need(t, what: str, dtype, shape, like=None):
         raise ValueError("%s is on %s, not on %s" % (what, t.device, like.device))
 
 
-def _run(name: str, entry, device, stream, *args):
-    """entry(*args, stream) with the tensors' device current; W4Error on a nonzero status."""
+def _placed(helper):
+    """Runs a helper with its first tensor's device current and, where ``stream``
+    is given, that stream: outputs and scratch are allocated on the stream that
+    writes them."""
+    @functools.wraps(helper)
+    def run(first, *args, stream=None, **kw):
+        import torch
+        if stream is not None:
+            if stream.device != first.device:
+                raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, first.device))
+            with torch.cuda.stream(stream):
+                return helper(first, *args, **kw)
+        if first.is_cuda and first.device.index != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return helper(first, *args, **kw)
+        return helper(first, *args, **kw)
+    return run
+
+
+def _run(name: str, entry, device, *args):
+    """entry(*args, current stream); W4Error on a nonzero status."""
     import torch
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _run(name, entry, device, stream, *args)
-    handle = (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
-    st = entry(*args, handle)
+    st = entry(*args, torch._C._cuda_getCurrentRawStream(device.index))
     if st != W4_OK:
         raise W4Error(st, name)
 
@@ -468,7 +490,8 @@ def _norm_checks(X, gamma, residual):
         _need(residual, "residual", torch.bfloat16, X.shape, X)
 
 
-def rmsnorm(X, gamma, eps: float, residual=None, out=None, stream=None):
+@_placed
+def rmsnorm(X, gamma, eps: float, residual=None, out=None):
     """RMS norm of the rows of X[M,K] (bf16 CUDA): returns (Y, H) in bf16 with
     h = X + residual, Y = h / sqrt(mean h^2 + eps) * gamma and H = h; H is None
     without a residual.  ``out`` = (Y, H): Y may be X, H may be X or the
@@ -482,12 +505,13 @@ def rmsnorm(X, gamma, eps: float, residual=None, out=None, stream=None):
         _need(Y, "out[0]", torch.bfloat16, X.shape, X)
         if H is not None:
             _need(H, "out[1]", torch.bfloat16, X.shape, X)
-    _run("w4_rmsnorm", lib().w4_rmsnorm, X.device, stream, X.data_ptr(), _addr(residual), gamma.data_ptr(),
+    _run("w4_rmsnorm", lib().w4_rmsnorm, X.device, X.data_ptr(), _addr(residual), gamma.data_ptr(),
          X.shape[0], X.shape[1], eps, _addr(H), Y.data_ptr(), None, None, MX_SCALES_ROWS)
     return Y, H
 
 
-def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SCALES_MMA, out=None, stream=None):
+@_placed
+def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SCALES_MMA, out=None):
     """``rmsnorm`` quantized to MXFP8 in the same pass: returns (codes uint8
     [M, K], scales uint8 in ``scale_layout`` as ``mxfp8_quant`` gives them, H).
     ``out`` = (codes, scales, H)."""
@@ -506,7 +530,7 @@ def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SC
         _need(scales, "out[1]", torch.uint8, (M, K // 32) if rows else (mx_scale_bytes(M, K),), X)
         if H is not None:
             _need(H, "out[2]", torch.bfloat16, X.shape, X)
-    _run("w4_rmsnorm", lib().w4_rmsnorm, X.device, stream, X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps,
+    _run("w4_rmsnorm", lib().w4_rmsnorm, X.device, X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps,
          _addr(H), None, codes.data_ptr(), scales.data_ptr(), scale_layout)
     return codes, scales, H
 
@@ -514,8 +538,9 @@ def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SC
 Routing = namedtuple("Routing", "ids weights offsets order pos")
 
 
+@_placed
 def route(logits, top_k: int, scoring: int = SOFTMAX, bias=None, n_groups: int = 1, topk_groups: int = 1,
-          group_top: int = 1, renormalize: bool = True, scale: float = 1.0, out=None, stream=None):
+          group_top: int = 1, renormalize: bool = True, scale: float = 1.0, out=None):
     """Routing of the tokens behind logits[T,E] (fp32 or bf16 CUDA) to top_k of
     E experts: a ``Routing`` of ids int32 [T, top_k], weights fp32 [T, top_k] and
     the plan of the experts' rows: offsets int32 [E + 1], order int32
@@ -541,21 +566,23 @@ def route(logits, top_k: int, scoring: int = SOFTMAX, bias=None, n_groups: int =
                                       (offsets, "offsets", torch.int32, (E + 1,)), (order, "order", torch.int32, (T * top_k,)),
                                       (pos, "pos", torch.int32, (T, top_k))):
             _need(t, what, dtype, shape, logits)
-    _run("w4_route", lib().w4_route, logits.device, stream, logits.data_ptr(), 1 if logits.dtype is torch.float32 else 0,
+    _run("w4_route", lib().w4_route, logits.device, logits.data_ptr(), 1 if logits.dtype is torch.float32 else 0,
          _addr(bias), T, E, top_k, scoring, n_groups, topk_groups, group_top, 1 if renormalize else 0, scale,
          ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), pos.data_ptr())
     return Routing(ids, weights, offsets, order, pos)
 
 
-def experts_gemm(X, qweight, scales, qzeros, group: int, mode: int, offsets, order=None, top_k: int = 1, out=None,
-                 stream=None):
+@_placed
+def experts_gemm(X, qweight, scales, qzeros, group: int, mode: int, offsets, order=None, top_k: int = 1,
+                 workspace=None, out=None):
     """The W4A16 product by expert: Y[i] = X[row] . W[e]^T for the sorted rows
     offsets[e] <= i < offsets[e + 1] of a ``route`` plan, row = order[i] // top_k
     (i itself without ``order``: X holds the sorted rows already).  qweight int32
     [E, N, K/8], scales fp16 [E, N, K/group] and qzeros int32 [E, N,
     ceil(K/group/8)] (None in SYM mode) are ``quant_pack``'s, stacked.  Returns
     Y bf16 [order.numel() or X.shape[0], N]; rows from offsets[E] on are not
-    written."""
+    written.  ``workspace``: w4a16_experts_workspace_bytes(...) bytes of CUDA
+    memory (allocated per call where it is needed and not given)."""
     import torch
     if X.dim() != 2 or qweight.dim() != 3 or group < 1:
         raise ValueError("X [R, K], qweight [E, N, K/8] and a group size are needed")
@@ -575,13 +602,21 @@ def experts_gemm(X, qweight, scales, qzeros, group: int, mode: int, offsets, ord
         out = torch.empty((P, N), dtype=torch.bfloat16, device=X.device)
     else:
         _need(out, "out", torch.bfloat16, (P, N), X)
-    _run("w4a16_experts_gemm", lib().w4a16_experts_gemm, X.device, stream, X.data_ptr(), R, offsets.data_ptr(),
+    if workspace is None and order is not None:
+        need = lib().w4a16_experts_workspace_bytes(P, E, K, 1)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
+    elif workspace is not None and (workspace.device != X.device or not workspace.is_contiguous()):
+        raise ValueError("workspace: a contiguous tensor on %s is needed" % X.device)
+    wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run("w4a16_experts_gemm", lib().w4a16_experts_gemm, X.device, X.data_ptr(), R, offsets.data_ptr(),
          _addr(order), top_k, E, P, N, K, qweight.data_ptr(), scales.data_ptr(), _addr(qzeros), group, mode,
-         out.data_ptr())
+         out.data_ptr(), _addr(workspace), wbytes)
     return out
 
 
-def combine(Y, pos, weights, add=None, out=None, stream=None):
+@_placed
+def combine(Y, pos, weights, add=None, out=None):
     """out[t] = add[t] + sum_j weights[t, j] * Y[pos[t, j]] (bf16 [T, N]) from an
     ``experts_gemm`` result Y[P, N] and a ``route`` plan's pos and weights
     [T, top_k]; positions of -1 add nothing.  ``out`` may be ``add``."""
@@ -598,6 +633,6 @@ def combine(Y, pos, weights, add=None, out=None, stream=None):
         out = torch.empty((T, N), dtype=torch.bfloat16, device=Y.device)
     else:
         _need(out, "out", torch.bfloat16, (T, N), Y)
-    _run("w4_combine", lib().w4_combine, Y.device, stream, Y.data_ptr(), P, pos.data_ptr(), weights.data_ptr(), T,
+    _run("w4_combine", lib().w4_combine, Y.device, Y.data_ptr(), P, pos.data_ptr(), weights.data_ptr(), T,
          top_k, N, _addr(add), out.data_ptr())
     return out

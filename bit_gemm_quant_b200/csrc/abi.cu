@@ -291,9 +291,21 @@ w4_status w4_route(const void *logits, int logits_type, const float *bias, int64
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 
+namespace {
+// Few rows an expert: the GEMV by expert; more: the tensor-core kernel.
+bool experts_run_gemv(int64_t P, int E) { return P <= 16 * (int64_t)E; }
+}  // namespace
+
+size_t w4a16_experts_workspace_bytes(int64_t P, int E, int64_t K, int gathered)
+{
+    if (P < 1 || E < 1 || K < 1 || !fits(P, K) || !gathered || experts_run_gemv(P, E)) return 0;
+    return w4::experts_tc_workspace_bytes(P, K);
+}
+
 w4_status w4a16_experts_gemm(const void *X, int64_t R, const int32_t *offsets, const int32_t *order, int top_k, int E,
                              int64_t P, int64_t N, int64_t K, const uint32_t *qweight, const void *scales,
-                             const uint32_t *qzeros, int group, int mode, void *Y, w4_stream_t stream)
+                             const uint32_t *qzeros, int group, int mode, void *Y, void *workspace,
+                             size_t workspace_bytes, w4_stream_t stream)
 {
     if (!X || !offsets || !qweight || !scales || !Y) return W4_ERR_INVALID_ARG;
     if (!group_ok(group) || !mode_ok(mode)) return W4_ERR_INVALID_ARG;
@@ -304,11 +316,15 @@ w4_status w4a16_experts_gemm(const void *X, int64_t R, const int32_t *offsets, c
     if (!aligned(X, 16) || !aligned(offsets, 4) || !aligned(order, 4) || !aligned(qweight, 16) || !aligned(scales, 2) ||
         !aligned(qzeros, 4) || !aligned(Y, 2))
         return W4_ERR_INVALID_ARG;
-    if (N * E > INT32_MAX - 256 || P > (1 << 30) || R > INT32_MAX || K > INT32_MAX) return W4_ERR_UNSUPPORTED;
+    const size_t need = w4a16_experts_workspace_bytes(P, E, K, order != nullptr);
+    if (need > workspace_bytes || (need > 0 && (!workspace || !aligned(workspace, 256)))) return W4_ERR_INVALID_ARG;
+    if (N * E > INT32_MAX - 256 || P > (1 << 23) || R > INT32_MAX || K > INT32_MAX) return W4_ERR_UNSUPPORTED;
     const w4::ExpertPlan plan = {offsets, order, order ? top_k : 1, E, (int)R, (int)P};
-    if (w4::max_units(P, E, 8) > 65535) return W4_ERR_UNSUPPORTED;
     const cudaError_t e =
-        w4::launch_experts_gemv(X, plan, N, K, qweight, scales, qzeros, group, mode, Y, (cudaStream_t)stream);
+        experts_run_gemv(P, E)
+            ? w4::launch_experts_gemv(X, plan, N, K, qweight, scales, qzeros, group, mode, Y, (cudaStream_t)stream)
+            : w4::launch_experts_tc(X, plan, N, K, qweight, scales, qzeros, group, mode, Y, workspace,
+                                    (cudaStream_t)stream);
     return e == cudaSuccess ? W4_OK : W4_ERR_CUDA;
 }
 

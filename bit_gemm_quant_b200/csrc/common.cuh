@@ -133,6 +133,10 @@ struct ExpertPlan;
 cudaError_t launch_experts_gemv(const void *X, const ExpertPlan &plan, int64_t N, int64_t K, const uint32_t *qweight,
                                 const void *scales, const uint32_t *qzeros, int group, int mode, void *Y,
                                 cudaStream_t stream);
+size_t experts_tc_workspace_bytes(int64_t P, int64_t K);
+cudaError_t launch_experts_tc(const void *X, ExpertPlan plan, int64_t N, int64_t K, const uint32_t *qweight,
+                              const void *scales, const uint32_t *qzeros, int group, int mode, void *Y, void *ws,
+                              cudaStream_t stream);
 cudaError_t launch_combine(const void *Y, int64_t P, const int *pos, const float *weights, int64_t T, int k, int64_t N,
                            const void *add, void *out, cudaStream_t stream);
 int read_and_clear_device_error();

@@ -44,6 +44,7 @@
 // the last CTA of a tile (found with an atomic counter) sums the partials in
 // split order, writes Y and re-zeroes the counter.
 #include "common.cuh"
+#include "experts.cuh"
 #include "tc_ptx.cuh"
 
 #include <cuda.h>
@@ -165,13 +166,18 @@ struct SlotData {
     uint32_t z0, z1;
 };
 
-template <int BN>
+// With EXP the product is w4a16_experts_gemm's: CTA (x, y) owns channels
+// 128 x .. of one expert and up to BN of that expert's rows (unit y of the
+// plan).  N and the channels are per expert, the arrays of the E weights follow
+// one another, and X holds the sorted rows.  A box's rows past the unit's are
+// other rows of X, whose accumulator columns are never stored.
+template <int BN, bool EXP>
 __global__ void __launch_bounds__(kThreads, TcCfg<BN>::kMinBlocks)
 gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_q,
                const __grid_constant__ CUtensorMap tmap_y, int y_tma, int M, int N, int K, int group_log2, int asym,
                const uint4 *__restrict__ qweight, const unsigned short *__restrict__ scales,
                const uint32_t *__restrict__ qzeros, void *__restrict__ Y, int y_f32, float *__restrict__ partial,
-               unsigned *__restrict__ counters, int splits, int kb_per_split, uint64_t wait_ns)
+               unsigned *__restrict__ counters, int splits, int kb_per_split, uint64_t wait_ns, ExpertPlan plan)
 {
     using C = TcCfg<BN>;
     constexpr int kStages = C::kStages;
@@ -191,7 +197,18 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     const uint64_t limit = wait_limit_of(wait_ns);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n0 = blockIdx.x * 128, m0 = blockIdx.y * BN, split = blockIdx.z;
+    const int n0 = blockIdx.x * 128, split = blockIdx.z;
+    int m0 = blockIdx.y * BN, q0 = n0;                                // first row of Y, first row of the code map
+    if (EXP) {
+        pdl_wait();                                                    // the plan is there
+        pdl_launch_dependents();
+        const ExpertUnit unit = find_unit(plan, blockIdx.y, BN);
+        if (unit.rows == 0) return;                                    // (every warp finds the same)
+        m0 = unit.row0;
+        M = m0 + unit.rows;
+        q0 = unit.expert * N + n0;
+        y_tma = y_tma && unit.rows == BN;                              // a whole tile, no other expert's rows
+    }
     const int KQ = K >> 5;                                            // 16-byte code chunks per channel
     const int kb_total = (K + kKB - 1) / kKB;
     const int kb_begin = split * kb_per_split;
@@ -215,8 +232,10 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();                                                       // the previous kernel's writes are visible
-    pdl_launch_dependents();
+    if (!EXP) {
+        pdl_wait();                                                    // the previous kernel's writes are visible
+        pdl_launch_dependents();
+    }
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer --
@@ -231,7 +250,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                     break;
                 mbar_arrive_expect_tx(&full_b[s], C::kStageBytes);
                 tma_load_2d(sB + s * C::kStageBytes, &tmap_x, &full_b[s], (kb_begin + i) * kKB, m0);
-                tma_load_2d(sB + s * C::kStageBytes + C::kBBytes, &tmap_q, &full_b[s], (kb_begin + i) * 8, n0);
+                tma_load_2d(sB + s * C::kStageBytes + C::kBBytes, &tmap_q, &full_b[s], (kb_begin + i) * 8, q0);
                 ++issued;
             }
             // drain: every issued copy must have landed before the CTA may exit
@@ -286,8 +305,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         const int r = 32 * q + lane;
         const int n = n0 + r;
         const bool okn = n < N;
-        const unsigned short *srow = scales + (size_t)(okn ? n : 0) * NG;
-        const uint32_t *zrow = qzeros + (size_t)(okn ? n : 0) * ZW;
+        const unsigned short *srow = scales + (size_t)(okn ? q0 + r : 0) * NG;
+        const uint32_t *zrow = qzeros + (size_t)(okn ? q0 + r : 0) * ZW;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16);
 
         // the codes arrive with the activations (TMA, full_b); only the scales
@@ -519,7 +538,7 @@ cudaError_t launch_bn(const CUtensorMap &map, const CUtensorMap &qmap, const CUt
     if (C::kMinBlocks == 2 && smem < 80 * 1024) smem = 80 * 1024;   // at most 2 CTAs share an SM's tensor memory
     static std::atomic<bool> attr_done[kMaxDevices];   // the attribute is per device
     {
-        const cudaError_t e = set_smem_attr(gemm_tc_kernel<BN>, (int)smem, attr_done);
+        const cudaError_t e = set_smem_attr(gemm_tc_kernel<BN, false>, (int)smem, attr_done);
         if (e != cudaSuccess) return e;
     }
     float *partial = nullptr;
@@ -530,9 +549,26 @@ cudaError_t launch_bn(const CUtensorMap &map, const CUtensorMap &qmap, const CUt
         counters = (unsigned *)((uint8_t *)ws + ((part + 255) & ~(size_t)255));
     }
     dim3 grid(p.n_tiles, p.m_tiles, p.splits);
-    return launch_pdl(gemm_tc_kernel<BN>, grid, dim3(kThreads), smem, stream, map, qmap, ymap, y_tma, M, N, K, glog2,
+    return launch_pdl(gemm_tc_kernel<BN, false>, grid, dim3(kThreads), smem, stream, map, qmap, ymap, y_tma, M, N, K, glog2,
                       asym, (const uint4 *)qweight, (const unsigned short *)scales, qzeros, Y, y_f32,
-                      partial, counters, p.splits, p.kb_per_split, wait_limit_ns());
+                      partial, counters, p.splits, p.kb_per_split, wait_limit_ns(), ExpertPlan{});
+}
+
+template <int BN>
+cudaError_t launch_experts_bn(const CUtensorMap &map, const CUtensorMap &qmap, const CUtensorMap &ymap, int y_tma,
+                              const ExpertPlan &plan, int N, int K, int glog2, int asym, const uint32_t *qweight,
+                              const void *scales, const uint32_t *qzeros, void *Y, cudaStream_t stream)
+{
+    using C = TcCfg<BN>;
+    size_t smem = 1024 + C::kStages * C::kStageBytes + 256;
+    if (C::kMinBlocks == 2 && smem < 80 * 1024) smem = 80 * 1024;   // at most 2 CTAs share an SM's tensor memory
+    static std::atomic<bool> attr_done[kMaxDevices];
+    const cudaError_t e = set_smem_attr(gemm_tc_kernel<BN, true>, (int)smem, attr_done);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((N + 127) / 128), (unsigned)max_units(plan.P, plan.E, BN));
+    return launch_pdl(gemm_tc_kernel<BN, true>, grid, dim3(kThreads), smem, stream, map, qmap, ymap, y_tma, 0, N, K,
+                      glog2, asym, (const uint4 *)qweight, (const unsigned short *)scales, qzeros, Y, 0,
+                      (float *)nullptr, (unsigned *)nullptr, 1, (K + kKB - 1) / kKB, wait_limit_ns(), plan);
 }
 
 }  // namespace
@@ -598,6 +634,80 @@ cudaError_t launch_gemm_tc(const void *X, int64_t M, int64_t N, int64_t K, const
     case 64: return launch_bn<64>(map, qmap, ymap, y_tma, p, (int)M, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, y_f32 ? 1 : 0, ws, stream);
     case 128: return launch_bn<128>(map, qmap, ymap, y_tma, p, (int)M, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, y_f32 ? 1 : 0, ws, stream);
     default: return launch_bn<256>(map, qmap, ymap, y_tma, p, (int)M, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, y_f32 ? 1 : 0, ws, stream);
+    }
+}
+
+// The rows of X in sorted order: dst[i] = X[order[i] / top_k] for i < offsets[E],
+// 16 bytes a thread and step.  The product's CTAs read each row N / 128 times, in
+// boxes of BN rows; TMA's four-row gather took about 50 cycles an instruction and
+// left the product at 232 TFLOP/s (8192 tokens, 2 of 8 experts of [14336, 4096]),
+// so the rows are moved once instead: 4 K bytes a row.
+__global__ void __launch_bounds__(256) sort_rows_kernel(const uint4 *X, ExpertPlan plan, int vecs, uint4 *dst)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const int rows = min(max(plan.offsets[plan.E], 0), plan.P);
+    const int64_t total = (int64_t)rows * vecs;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int row = (int)(i / vecs), v = (int)(i - (int64_t)row * vecs);
+        dst[i] = X[(int64_t)expert_x_row(plan, row) * vecs + v];
+    }
+}
+
+size_t experts_tc_workspace_bytes(int64_t P, int64_t K) { return (size_t)P * K * 2; }
+
+cudaError_t launch_experts_tc(const void *X, ExpertPlan plan, int64_t N, int64_t K, const uint32_t *qweight,
+                              const void *scales, const uint32_t *qzeros, int group, int mode, void *Y, void *ws,
+                              cudaStream_t stream)
+{
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    if (plan.order) {
+        const int64_t want = (plan.P * (K / 8) + 255) / 256;
+        const unsigned grid = (unsigned)(want < (int64_t)kNumSMs * 16 ? want : (int64_t)kNumSMs * 16);
+        const cudaError_t e = launch_pdl(sort_rows_kernel, dim3(grid), dim3(256), 0, stream, (const uint4 *)X, plan,
+                                         (int)(K / 8), (uint4 *)ws);
+        if (e != cudaSuccess) return e;
+        X = ws;
+        plan.order = nullptr;
+    }
+    const int64_t rows = plan.P / plan.E;
+    const int BN = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    CUtensorMap map, qmap, ymap;
+    const cuuint64_t gdim[2] = {(cuuint64_t)K, (cuuint64_t)plan.P};
+    const cuuint64_t gstride[1] = {(cuuint64_t)K * 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kKB, (cuuint32_t)BN};
+    const cuuint32_t estride[2] = {1, 1};
+    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(X), gdim, gstride, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    const cuuint64_t qdim[2] = {(cuuint64_t)(K / 8), (cuuint64_t)(plan.E * N)};
+    const cuuint64_t qstride[1] = {(cuuint64_t)K / 2};
+    const cuuint32_t qbox[2] = {8u, 128u};
+    if (enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint32_t *>(qweight), qdim, qstride, qbox, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    ymap = map;
+    int y_tma = 0;
+    if (((uintptr_t)Y % 16) == 0 && (N * 2) % 16 == 0) {
+        const cuuint64_t ydim[2] = {(cuuint64_t)N, (cuuint64_t)plan.P};
+        const cuuint64_t ystride[1] = {(cuuint64_t)N * 2};
+        const cuuint32_t ybox[2] = {128u, (cuuint32_t)BN};
+        if (enc(&ymap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y, ydim, ystride, ybox, estride,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+        y_tma = 1;
+    }
+    const int glog2 = group == 32 ? 5 : group == 64 ? 6 : 7;
+    const int asym = mode == W4_ASYM;
+    switch (BN) {
+    case 32: return launch_experts_bn<32>(map, qmap, ymap, y_tma, plan, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, stream);
+    case 64: return launch_experts_bn<64>(map, qmap, ymap, y_tma, plan, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, stream);
+    case 128: return launch_experts_bn<128>(map, qmap, ymap, y_tma, plan, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, stream);
+    default: return launch_experts_bn<256>(map, qmap, ymap, y_tma, plan, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, stream);
     }
 }
 

@@ -489,6 +489,15 @@ w4_status w4_route(const void *logits, int logits_type, const float *bias, int64
                    float *weights, int32_t *offsets, int32_t *order, int32_t *pos, w4_stream_t stream);
 
 /*
+ * w4a16_experts_workspace_bytes -- device scratch that w4a16_experts_gemm
+ * needs (0 if none): the rows of X in sorted order, 2 * P * K bytes, where the
+ * rows come through `order` (gathered != 0) and the product runs on the tensor
+ * cores.  Contents need not be initialised and hold nothing between calls;
+ * calls that may run at the same time need one each.
+ */
+size_t w4a16_experts_workspace_bytes(int64_t P, int E, int64_t K, int gathered);
+
+/*
  * w4a16_experts_gemm -- w4a16_gemm for the rows of many experts at once:
  *   Y[i] = X[row(i)] . W^[e(i)]^T     for i < offsets[E], offsets[e] <= i < offsets[e + 1],
  * with row(i) = order[i] / top_k, or i when order is NULL, and W^ dequantized
@@ -509,18 +518,21 @@ w4_status w4_route(const void *logits, int logits_type, const float *bias, int64
  *   mode     W4_SYM or W4_ASYM; no flags.
  *   Y        out, bf16 [P][N], 2-byte aligned.  The rows from offsets[E] on
  *            are left as they were.
+ *   workspace, workspace_bytes: device scratch of at least
+ *            w4a16_experts_workspace_bytes(P, E, K, order != NULL) bytes (may
+ *            be NULL when that is 0); 256-byte aligned.
  * The plan stays on the device: nothing of the call depends on the host
  * knowing it, so the call can be captured and replayed with other plans of the
  * same P.  Values of offsets outside [0, P] are taken as the nearest of the
  * two and rows outside [0, R) as its ends, so a wrong plan gives wrong rows of
  * Y, never an access outside the arrays.  Errors as for w4a16_gemm;
- * W4_ERR_UNSUPPORTED for shapes past 32-bit indexing (E * N, P, R, K, and the
- * number of tiles).  Needs no workspace.  Asynchronous on `stream`; results
- * repeat bit for bit.
+ * W4_ERR_UNSUPPORTED for P above 2^23 and for shapes past 32-bit indexing
+ * (E * N, R, K).  Asynchronous on `stream`; results repeat bit for bit.
  */
 w4_status w4a16_experts_gemm(const void *X, int64_t R, const int32_t *offsets, const int32_t *order, int top_k, int E,
                              int64_t P, int64_t N, int64_t K, const uint32_t *qweight, const void *scales,
-                             const uint32_t *qzeros, int group, int mode, void *Y, w4_stream_t stream);
+                             const uint32_t *qzeros, int group, int mode, void *Y, void *workspace,
+                             size_t workspace_bytes, w4_stream_t stream);
 
 /*
  * w4_combine -- the weighted sum over each token's experts:

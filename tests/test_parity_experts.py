@@ -253,8 +253,8 @@ FAKE = 1 << 20
 
 
 def call(w4, X=FAKE, R=64, offsets=FAKE, order=FAKE, k=2, E=8, P=64, N=64, K=256, q=FAKE, s=FAKE, z=None, g=128, mode=0,
-         Y=FAKE):
-    return w4.w4a16_experts_gemm(X, R, offsets, order, k, E, P, N, K, q, s, z, g, mode, Y, None)
+         Y=FAKE, ws=None, wbytes=0):
+    return w4.w4a16_experts_gemm(X, R, offsets, order, k, E, P, N, K, q, s, z, g, mode, Y, ws, wbytes, None)
 
 
 @pytest.mark.parametrize("bad", [
@@ -262,14 +262,24 @@ def call(w4, X=FAKE, R=64, offsets=FAKE, order=FAKE, k=2, E=8, P=64, N=64, K=256
     dict(E=1025), dict(P=0), dict(N=0), dict(K=0), dict(K=192), dict(g=16), dict(mode=2), dict(mode=0x100),
     dict(mode=0x201), dict(mode=1), dict(z=FAKE), dict(order=None, R=63), dict(X=FAKE + 8), dict(q=FAKE + 4),
     dict(s=FAKE + 1), dict(offsets=FAKE + 2), dict(order=FAKE + 2), dict(mode=1, z=FAKE + 2), dict(Y=FAKE + 1),
-    dict(N=1 << 61)])
+    dict(N=1 << 61), dict(P=4096, ws=FAKE, wbytes=4096 * 512 - 1), dict(P=4096, wbytes=4096 * 512),
+    dict(P=4096, ws=FAKE + 128, wbytes=4096 * 512)])
 def test_refusals(w4, bad):
     assert call(w4, **bad) == w4.W4_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("big", [dict(N=1 << 29), dict(P=(1 << 30) + 1), dict(R=1 << 31, order=FAKE)])
+@pytest.mark.parametrize("big", [dict(N=1 << 29), dict(P=(1 << 23) + 1, ws=FAKE, wbytes=1 << 40),
+                                 dict(R=1 << 31, order=FAKE)])
 def test_unsupported(w4, big):
     assert call(w4, **big) == w4.W4_ERR_UNSUPPORTED
+
+
+def test_workspace_bytes(w4):
+    assert w4.w4a16_experts_workspace_bytes(4096, 8, 256, 1) == 4096 * 512
+    assert w4.w4a16_experts_workspace_bytes(4096, 8, 256, 0) == 0       # the rows are sorted already
+    assert w4.w4a16_experts_workspace_bytes(8, 8, 256, 1) == 0          # the GEMV reads them in place
+    assert w4.w4a16_experts_workspace_bytes(0, 8, 256, 1) == 0
+    assert w4.w4a16_experts_workspace_bytes(1 << 40, 8, 1 << 40, 1) == 0
 
 
 def test_helper_refusals(w4):
