@@ -130,9 +130,9 @@ cudaError_t launch_route(const void *logits, int f32, const float *bias, int64_t
                          int groups, int keep, int group_top, int renorm, float scale, int *ids, float *weights,
                          int *offsets, int *order, int *pos, cudaStream_t stream);
 struct ExpertPlan;
-cudaError_t launch_experts_gemv(const void *X, const ExpertPlan &plan, int64_t N, int64_t K, const uint32_t *qweight,
-                                const void *scales, const uint32_t *qzeros, int group, int mode, void *Y,
-                                cudaStream_t stream);
+cudaError_t launch_experts_stream(const void *X, const ExpertPlan &plan, int64_t N, int64_t K, const uint32_t *qweight,
+                                  const void *scales, const uint32_t *qzeros, int group, int mode, void *Y,
+                                  cudaStream_t stream);
 size_t experts_tc_workspace_bytes(int64_t P, int64_t K);
 cudaError_t launch_experts_tc(const void *X, ExpertPlan plan, int64_t N, int64_t K, const uint32_t *qweight,
                               const void *scales, const uint32_t *qzeros, int group, int mode, void *Y, void *ws,

@@ -672,7 +672,7 @@ cudaError_t launch_experts_tc(const void *X, ExpertPlan plan, int64_t N, int64_t
         plan.order = nullptr;
     }
     const int64_t rows = plan.P / plan.E;
-    const int BN = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+    const int BN = rows <= 20 ? 32 : rows <= 48 ? 64 : rows <= 400 ? 128 : 256;
     CUtensorMap map, qmap, ymap;
     const cuuint64_t gdim[2] = {(cuuint64_t)K, (cuuint64_t)plan.P};
     const cuuint64_t gstride[1] = {(cuuint64_t)K * 2};

@@ -62,7 +62,6 @@
 // an error code (read by w4_device_error), and the warp stops computing, waits
 // (again bounded) for its own copies in flight and returns.
 #include "common.cuh"
-#include "experts.cuh"
 #include "tc_ptx.cuh"
 
 namespace w4 {
@@ -128,17 +127,12 @@ __device__ __forceinline__ uint4 const_word(unsigned short s16bits, uint32_t zp)
     return make_uint4(c.shi, c.slo, c.z, 0u);
 }
 
-// With EXP the product is w4a16_experts_gemm's: CTA (x, y) owns the 16-channel
-// tile x of one expert and up to 8 * MT of that expert's rows (unit y of the
-// plan); N and the tile are per expert, the arrays of the E weights follow one
-// another, and a token's activations are the row of X that the plan names.
-template <int G, int MODE, int MT, int NW, int SK, int R, int MINB, bool EARLY, bool XPF, bool EXP>
+template <int G, int MODE, int MT, int NW, int SK, int R, int MINB, bool EARLY, bool XPF>
 __global__ void __launch_bounds__(NW * 32, MINB)
 gemv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *__restrict__ X, int M, int N, int K,
             const unsigned short *__restrict__ scales, const uint32_t *__restrict__ qzeros,
-            void *__restrict__ Y, int yflags, int *err, uint64_t wait_ns, ExpertPlan plan)
+            void *__restrict__ Y, int yflags, int *err, uint64_t wait_ns)
 {
-    static_assert(!(EXP && EARLY), "the plan names the weights: nothing can be read before it");
     // bit 0: fp32 Y (W4_OUT_F32); bit 1: codes in the repacked layout
     // (w4_repack: 2 KB boxes stored contiguously, the tensor map is 4-D)
     const int y_f32 = yflags & 1;
@@ -178,16 +172,6 @@ gemv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *__r
         pdl_wait();                                   // the previous kernel's writes are visible
         pdl_launch_dependents();
     }
-    int q_row = r0, y_row = 0;                        // the tile's first row in the code map, and its first row of Y
-    if (EXP) {
-        const ExpertUnit unit = find_unit(plan, blockIdx.y, 8 * MT);
-        if (unit.rows == 0) return;                   // (every warp finds the same)
-        M = unit.rows;
-        y_row = unit.row0;
-        q_row = unit.expert * N + r0;
-        scales += (size_t)unit.expert * N * NG;
-        if (MODE == W4_ASYM) qzeros += (size_t)unit.expert * N * ZW;
-    }
 
     auto issue = [&](int i) {                         // lane 0: stage i of this warp into slot i % R
         const int s = i % R;
@@ -207,7 +191,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *__r
                 asm volatile(
                     "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
                     "%4}], [%2];" ::"r"(ring_s + s * C::kStageBytes + bb * C::kBoxBytes),
-                    "l"(&tmap_q), "r"(bar0 + 8 * s), "r"((sb * C::kBoxes + bb) * 32), "r"(q_row)
+                    "l"(&tmap_q), "r"(bar0 + 8 * s), "r"((sb * C::kBoxes + bb) * 32), "r"(r0)
                     : "memory");
         }
     };
@@ -245,11 +229,7 @@ gemv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *__r
     const uint4 *clane = cslot + g + 16 * lane_gl;    // constants of row g (row g + 8: + 8)
     const __nv_bfloat16 *xrow[MT];                   // a token past M reads token M-1
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        int row = min(g + 8 * mt, M - 1);
-        if (EXP) row = expert_x_row(plan, y_row + row);
-        xrow[mt] = X + (size_t)row * K + t * 32;
-    }
+    for (int mt = 0; mt < MT; ++mt) xrow[mt] = X + (size_t)min(g + 8 * mt, M - 1) * K + t * 32;
 
     // activations of chunk h of stage sb: 4 x 16 bytes per token group.  In a
     // stage that runs past the end of K (K is a multiple of 32, chunks are
@@ -366,10 +346,10 @@ gemv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *__r
                 for (int e = 0; e < 4; ++e)
                     sm[e] += ((const float(*)[4 * MT])(smem + w * R * C::kStageBytes))[lane][4 * mt + e];
             const int m0 = 8 * mt + 2 * t, m1 = m0 + 1;   // tokens of c0/c2 and c1/c3
-            if (rA < N && m0 < M) store_y(Y, (size_t)(y_row + m0) * N + rA, sm[0], y_f32);
-            if (rA < N && m1 < M) store_y(Y, (size_t)(y_row + m1) * N + rA, sm[1], y_f32);
-            if (rB < N && m0 < M) store_y(Y, (size_t)(y_row + m0) * N + rB, sm[2], y_f32);
-            if (rB < N && m1 < M) store_y(Y, (size_t)(y_row + m1) * N + rB, sm[3], y_f32);
+            if (rA < N && m0 < M) store_y(Y, (size_t)m0 * N + rA, sm[0], y_f32);
+            if (rA < N && m1 < M) store_y(Y, (size_t)m1 * N + rA, sm[1], y_f32);
+            if (rB < N && m0 < M) store_y(Y, (size_t)m0 * N + rB, sm[2], y_f32);
+            if (rB < N && m1 < M) store_y(Y, (size_t)m1 * N + rB, sm[3], y_f32);
         }
     }
 }
@@ -381,44 +361,12 @@ cudaError_t launch_cfg(const CUtensorMap &map, const void *X, int64_t M, int64_t
     const int64_t blocks = (N + 15) / 16;             // one 16-channel tile per CTA
     constexpr int smem = GemvCfg<G, SK, NW, R, MT>::kBytes;
     static std::atomic<bool> attr_done[kMaxDevices];
-    auto kern = gemv_kernel<G, MODE, MT, NW, SK, R, MINB, EARLY, XPF, false>;
+    auto kern = gemv_kernel<G, MODE, MT, NW, SK, R, MINB, EARLY, XPF>;
     const cudaError_t e = set_smem_attr(kern, smem, attr_done);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3((unsigned)blocks), dim3(NW * 32), smem, stream, map, (const __nv_bfloat16 *)X,
                       (int)M, (int)N, (int)K, (const unsigned short *)scales, qzeros, Y, y_f32, err,
-                      wait_limit_ns(), ExpertPlan{});
-}
-
-// The same kernel by expert: a 2-D grid of channel tiles and units of 8 * MT rows.
-template <int G, int MODE, int MT>
-cudaError_t launch_experts_g(const CUtensorMap &map, const void *X, const ExpertPlan &plan, int64_t N, int64_t K,
-                             const void *scales, const uint32_t *qzeros, void *Y, int *err, cudaStream_t stream)
-{
-    constexpr int NW = 4, SK = 512, R = 2, MINB = MT == 1 ? 5 : 4;
-    constexpr int smem = GemvCfg<G, SK, NW, R, MT>::kBytes;
-    static std::atomic<bool> attr_done[kMaxDevices];
-    auto kern = gemv_kernel<G, MODE, MT, NW, SK, R, MINB, false, false, true>;
-    const cudaError_t e = set_smem_attr(kern, smem, attr_done);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((N + 15) / 16), (unsigned)max_units(plan.P, plan.E, 8 * MT));
-    return launch_pdl(kern, grid, dim3(NW * 32), smem, stream, map, (const __nv_bfloat16 *)X, 0, (int)N, (int)K,
-                      (const unsigned short *)scales, qzeros, Y, 0, err, wait_limit_ns(), plan);
-}
-
-template <int MT>
-cudaError_t launch_experts_mt(const CUtensorMap &map, const void *X, const ExpertPlan &plan, int64_t N, int64_t K,
-                              const void *scales, const uint32_t *qzeros, int group, int mode, void *Y, int *err,
-                              cudaStream_t stream)
-{
-    switch (group * 2 + mode) {
-    case 32 * 2 + W4_SYM: return launch_experts_g<32, W4_SYM, MT>(map, X, plan, N, K, scales, qzeros, Y, err, stream);
-    case 32 * 2 + W4_ASYM: return launch_experts_g<32, W4_ASYM, MT>(map, X, plan, N, K, scales, qzeros, Y, err, stream);
-    case 64 * 2 + W4_SYM: return launch_experts_g<64, W4_SYM, MT>(map, X, plan, N, K, scales, qzeros, Y, err, stream);
-    case 64 * 2 + W4_ASYM: return launch_experts_g<64, W4_ASYM, MT>(map, X, plan, N, K, scales, qzeros, Y, err, stream);
-    case 128 * 2 + W4_SYM: return launch_experts_g<128, W4_SYM, MT>(map, X, plan, N, K, scales, qzeros, Y, err, stream);
-    case 128 * 2 + W4_ASYM: return launch_experts_g<128, W4_ASYM, MT>(map, X, plan, N, K, scales, qzeros, Y, err, stream);
-    default: return cudaErrorInvalidValue;
-    }
+                      wait_limit_ns());
 }
 
 // Launch shape by tile count (16 channels per tile), chosen from timings on
@@ -529,21 +477,6 @@ cudaError_t launch_gemv(const void *X, int64_t M, int64_t N, int64_t K, const ui
                               : launch_mt<1, false>(map, X, M, N, K, scales, qzeros, group, mode, Y, (y_f32 ? 1 : 0) | (repacked ? 2 : 0), err, stream);
     return weights_static ? launch_mt<2, true>(map, X, M, N, K, scales, qzeros, group, mode, Y, (y_f32 ? 1 : 0) | (repacked ? 2 : 0), err, stream)
                           : launch_mt<2, false>(map, X, M, N, K, scales, qzeros, group, mode, Y, (y_f32 ? 1 : 0) | (repacked ? 2 : 0), err, stream);
-}
-
-cudaError_t launch_experts_gemv(const void *X, const ExpertPlan &plan, int64_t N, int64_t K, const uint32_t *qweight,
-                                const void *scales, const uint32_t *qzeros, int group, int mode, void *Y,
-                                cudaStream_t stream)
-{
-    int *err = device_error_word();
-    if (!err) return cudaErrorUnknown;
-    CUtensorMap map;
-    const cudaError_t e = gemv_code_map(&map, qweight, (int64_t)plan.E * N, K, false);
-    if (e != cudaSuccess) return e;
-    // 8 rows a unit while an expert has 8 on average at most
-    if (plan.P <= 8 * (int64_t)plan.E)
-        return launch_experts_mt<1>(map, X, plan, N, K, scales, qzeros, group, mode, Y, err, stream);
-    return launch_experts_mt<2>(map, X, plan, N, K, scales, qzeros, group, mode, Y, err, stream);
 }
 
 }  // namespace w4

@@ -178,13 +178,11 @@ struct GroupConst {
 __device__ __forceinline__ GroupConst group_const(unsigned short s16bits, uint32_t zp)
 {
     const float sf = __half2float(__ushort_as_half(s16bits));
-    const __nv_bfloat16 hi = __float2bfloat16_rn(sf);
-    const __nv_bfloat16 lo = __float2bfloat16_rn(sf - __bfloat162float(hi));
-    const uint32_t h = __bfloat16_as_ushort(hi), l = __bfloat16_as_ushort(lo);
-    GroupConst gc;
-    gc.shi = h | (h << 16);
-    gc.slo = l | (l << 16);
-    gc.z = 0xC300C300u | (zp << 16) | zp;   // -(128 + zp)
+    GroupConst gc;                           // (the pair conversion rounds and duplicates at once)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(gc.shi) : "f"(sf));
+    const float rest = sf - __uint_as_float(gc.shi << 16);
+    asm("cvt.rn.bf16x2.f32 %0, %1, %1;" : "=r"(gc.slo) : "f"(rest));
+    gc.z = 0xC300C300u + zp * 0x00010001u;   // -(128 + zp)
     return gc;
 }
 
