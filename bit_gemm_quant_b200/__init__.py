@@ -556,10 +556,8 @@ def route(logits, top_k: int, scoring: int = SOFTMAX, bias=None, n_groups: int =
         _need(bias, "bias", torch.float32, (E,), logits)
     if out is None:
         ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=logits.device)
-        order = torch.empty(T * top_k, dtype=torch.int32, device=logits.device)
-        pos = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty_like(ids, dtype=torch.float32)
+        offsets, order, pos = ids.new_empty(E + 1), ids.new_empty(T * top_k), torch.empty_like(ids)
     else:
         ids, weights, offsets, order, pos = out
         for t, what, dtype, shape in ((ids, "ids", torch.int32, (T, top_k)), (weights, "weights", torch.float32, (T, top_k)),

@@ -17,6 +17,10 @@
 // within a thread, then a butterfly over the warp, then over the CTA's warps
 // through shared memory, always in the same order.
 //
+// What bounds it: HBM.  8192 rows of 8192, residual, MXFP8 out (472 MB): 77 us,
+// 6.1 TB/s, 93% of the measured copy rate; with x and r loaded one after the
+// other 110.  One row of 4096: 1.8 us in a graph, launch and latency.
+//
 // Rounding: everything between the bf16 inputs and the outputs is fp32.  h is
 // rounded to bf16 for H alone; the norm uses the fp32 sum, and the codes are
 // rounded from the fp32 y, so no output carries a second rounding.
@@ -32,7 +36,7 @@ struct NormArgs {
     __nv_bfloat16 *h, *y;
     uint8_t *codes, *scales;
     int64_t M;
-    int K, mma;
+    int K, mma, sf_words;   // sf_words: scales leave in 32-bit words
     float eps;
 };
 
@@ -78,8 +82,11 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
 }
 
 // Rows of 16-byte vectors.  `warps` warps share a row: 1 (each warp of the CTA
-// has a row of its own) or all of the CTA's.
-template <int VPT>
+// has a row of its own) or all of the CTA's.  With SHIFT rows are no whole
+// vectors: a row begins `o` elements behind a vector's start, its vectors are
+// those that hold any of it, elements of other rows count as 0 and are not
+// written (bf16 out only).
+template <int VPT, bool SHIFT>
 __global__ void __launch_bounds__(1024 / (VPT > 2 ? 2 : 1)) rmsnorm_vec_kernel(NormArgs a, int64_t rows, int warps)
 {
     pdl_wait();
@@ -88,50 +95,74 @@ __global__ void __launch_bounds__(1024 / (VPT > 2 ? 2 : 1)) rmsnorm_vec_kernel(N
     const int t = warps == 1 ? (threadIdx.x & 31) : threadIdx.x;
     const int64_t row = warps == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= rows) return;                          // (whole warps, and with warps > 1 whole CTAs)
-    const int nv = a.K >> 3;                          // vectors of a row
     if (row >= a.M) {                                 // pads the last band of the tensor-core layout
-        for (int kb = t; kb < a.K >> 5; kb += threads) a.scales[mma_sf_offset(row, kb, a.K)] = 0;
+        for (int kb = 4 * t; kb < a.K >> 5; kb += 4 * threads) *(uint32_t *)(a.scales + mma_sf_offset(row, kb, a.K)) = 0u;
         return;
     }
-    const uint4 *x = (const uint4 *)a.x + row * nv;
-    const uint4 *r = (const uint4 *)a.r + row * nv;
+    const int o = SHIFT ? (int)((row * a.K) & 7) : 0;
+    const int nv = SHIFT ? (o + a.K + 7) >> 3 : a.K >> 3;   // vectors of a row
+    const int64_t v0 = (row * a.K) >> 3;                    // the first
+    const int64_t whole = SHIFT ? (a.M * a.K) >> 3 : 0;     // vectors that lie inside the arrays
+    auto load = [&](const __nv_bfloat16 *p, int v) {
+        if (v >= nv) return make_uint4(0u, 0u, 0u, 0u);
+        if (!SHIFT || v0 + v < whole) return ((const uint4 *)p)[v0 + v];
+        uint32_t w[4] = {0u, 0u, 0u, 0u};                   // the arrays end inside this vector
+        for (int64_t e = (v0 + v) * 8; e < a.M * a.K; ++e)
+            w[(e & 7) >> 1] |= (uint32_t)__bfloat16_as_ushort(p[e]) << (16 * (e & 1));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    };
+    auto store = [&](__nv_bfloat16 *p, int v, const float (&f)[8]) {
+        const int k = 8 * v - o;
+        if (!SHIFT || (k >= 0 && k + 8 <= a.K)) ((uint4 *)p)[v0 + v] = pack8(f);
+        else
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k + j >= 0 && k + j < a.K) p[row * a.K + k + j] = __float2bfloat16_rn(f[j]);
+    };
     float f[VPT][8];
     float ss = 0.f;
+    uint4 xv[VPT], rv[VPT];                                 // (all in flight before any is looked at)
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int v = t + i * threads;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (v < nv) u = x[v];
-        unpack8(u, f[i]);
+        xv[i] = load(a.x, t + i * threads);
+        rv[i] = a.r ? load(a.r, t + i * threads) : make_uint4(0u, 0u, 0u, 0u);
     }
-    if (a.r) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = t + i * threads;
-            uint4 u = make_uint4(0u, 0u, 0u, 0u);
-            if (v < nv) u = r[v];
-            float g[8];
-            unpack8(u, g);
+    for (int i = 0; i < VPT; ++i) {
+        float g[8];
+        unpack8(xv[i], f[i]);
+        unpack8(rv[i], g);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] += g[j];
-        }
+        for (int j = 0; j < 8; ++j) f[i][j] += g[j];
     }
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(f[i][j], f[i][j], ss);
+        for (int j = 0; j < 8; ++j) {
+            const int k = 8 * (t + i * threads) - o + j;
+            if (SHIFT && (k < 0 || k >= a.K)) f[i][j] = 0.f;
+            ss = fmaf(f[i][j], f[i][j], ss);
+        }
     const float inv = 1.0f / sqrtf(row_sum(ss, warps) / (float)a.K + a.eps);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = t + i * threads;
         const bool in = v < nv;
-        if (a.h && in) ((uint4 *)a.h)[row * nv + v] = pack8(f[i]);
+        if (a.h && in) store(a.h, v, f[i]);
         float g[8];
-        unpack8(in ? __ldg((const uint4 *)a.gamma + v) : make_uint4(0u, 0u, 0u, 0u), g);
+        if (SHIFT) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = 8 * v - o + j;
+                g[j] = k >= 0 && k < a.K ? __bfloat162float(__ldg(a.gamma + k)) : 0.f;
+            }
+        } else {
+            unpack8(in ? __ldg((const uint4 *)a.gamma + v) : make_uint4(0u, 0u, 0u, 0u), g);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * inv * g[j];
-        if (a.y && in) ((uint4 *)a.y)[row * nv + v] = pack8(f[i]);
-        if (a.codes) {
+        if (a.y && in) store(a.y, v, f[i]);
+        if (!SHIFT && a.codes) {
             // amax as bit patterns (integer order = order of magnitudes), over the block's four threads
             uint32_t m = 0;
 #pragma unroll
@@ -149,20 +180,24 @@ __global__ void __launch_bounds__(1024 / (VPT > 2 ? 2 : 1)) rmsnorm_vec_kernel(N
                     make_float2(f[i][4 * j + 2] * sc, f[i][4 * j + 3] * sc), __NV_SATFINITE, __NV_E4M3);
                 q[j] = (uint32_t)lo | ((uint32_t)hi << 16);
             }
-            if (in) {
-                ((uint2 *)a.codes)[row * nv + v] = make_uint2(q[0], q[1]);
-                if ((v & 3) == 0) {
-                    const int kb = v >> 2;
-                    const int64_t at = a.mma ? mma_sf_offset(row, kb, a.K) : row * (a.K >> 5) + kb;
-                    a.scales[at] = (uint8_t)e8;
-                }
+            if (in) ((uint2 *)a.codes)[row * nv + v] = make_uint2(q[0], q[1]);
+            const int kb = v >> 2;
+            if (a.sf_words) {
+                // four blocks' scales (16 lanes) as one word
+                uint32_t word = (uint32_t)e8 << (8 * (kb & 3));
+                word |= __shfl_xor_sync(0xffffffffu, word, 4);
+                word |= __shfl_xor_sync(0xffffffffu, word, 8);
+                if (in && (v & 15) == 0)
+                    *(uint32_t *)(a.scales + (a.mma ? mma_sf_offset(row, kb, a.K) : row * (a.K >> 5) + kb)) = word;
+            } else if (in && (v & 3) == 0) {
+                a.scales[row * (a.K >> 5) + kb] = (uint8_t)e8;
             }
         }
     }
 }
 
-// Rows that are no whole vectors, or pointers that are not 16-byte aligned:
-// one element per thread and step, bf16 out only.
+// Pointers that are not 16-byte aligned: one element per thread and step, bf16
+// out only.
 __global__ void __launch_bounds__(1024) rmsnorm_any_kernel(NormArgs a)
 {
     pdl_wait();
@@ -192,32 +227,44 @@ __global__ void __launch_bounds__(1024) rmsnorm_any_kernel(NormArgs a)
     }
 }
 
+// Threads for nv vectors a row.  Few rows: a vector a thread, so that a row's
+// latency is one load deep.  Many rows: four, so that a resident CTA has more
+// bytes on their way (8192 rows of 8192, MXFP8 out, residual: 77 us with four,
+// 99 with two); rows of up to 128 vectors then have a warp each.
+template <bool SHIFT>
+cudaError_t launch_vec(const NormArgs &a, int64_t rows, int nv, cudaStream_t stream)
+{
+    const bool many = rows > 2 * kNumSMs;
+    const int vpt = many ? (nv <= 32 ? 1 : nv <= 64 ? 2 : 4) : nv <= 1024 ? 1 : nv <= 2048 ? 2 : 4;
+    int warps = (nv + 32 * vpt - 1) / (32 * vpt);
+    const int per_cta = warps == 1 ? 8 : 1;           // rows
+    if (nv > 2048) {                                  // 512 threads; a shifted row of 32767 has 4097 vectors
+        constexpr int kLong = SHIFT ? 9 : 8;
+        warps = (nv + 32 * kLong - 1) / (32 * kLong);
+        return launch_pdl(rmsnorm_vec_kernel<kLong, SHIFT>, dim3((unsigned)rows), dim3(warps * 32), 0, stream, a, rows, warps);
+    }
+    const dim3 grid((unsigned)((rows + per_cta - 1) / per_cta)), block(warps * per_cta * 32);
+    if (vpt == 1) return launch_pdl(rmsnorm_vec_kernel<1, SHIFT>, grid, block, 0, stream, a, rows, warps);
+    if (vpt == 2) return launch_pdl(rmsnorm_vec_kernel<2, SHIFT>, grid, block, 0, stream, a, rows, warps);
+    return launch_pdl(rmsnorm_vec_kernel<4, SHIFT>, grid, block, 0, stream, a, rows, warps);
+}
+
 }  // namespace
 
 cudaError_t launch_rmsnorm(const void *X, const void *residual, const void *gamma, int64_t M, int64_t K, float eps,
                            void *H, void *Y, uint8_t *codes, uint8_t *scales, int layout, cudaStream_t stream)
 {
+    const int mma = codes && layout == W4_MX_SCALES_MMA;
     NormArgs a = {(const __nv_bfloat16 *)X, (const __nv_bfloat16 *)residual, (const __nv_bfloat16 *)gamma,
                   (__nv_bfloat16 *)H, (__nv_bfloat16 *)Y, codes, scales, M, (int)K,
-                  codes && layout == W4_MX_SCALES_MMA, eps};
+                  mma, K % 128 == 0 && (uintptr_t)scales % 4 == 0, eps};
     const uintptr_t all = (uintptr_t)X | (uintptr_t)residual | (uintptr_t)gamma | (uintptr_t)H | (uintptr_t)Y;
-    if (K % 8 != 0 || all % 16 != 0) {
+    if (all % 16 != 0) {
         const int threads = K >= 1024 ? 1024 : (int)((K + 31) / 32 * 32);
         return launch_pdl(rmsnorm_any_kernel, dim3((unsigned)M), dim3(threads), 0, stream, a);
     }
-    const int64_t rows = a.mma ? mx_padded_rows(M) : M;
-    const int nv = (int)(K / 8);
-    if (nv <= 64) {
-        const dim3 grid((unsigned)((rows + 7) / 8));
-        if (nv <= 32) return launch_pdl(rmsnorm_vec_kernel<1>, grid, dim3(256), 0, stream, a, rows, 1);
-        return launch_pdl(rmsnorm_vec_kernel<2>, grid, dim3(256), 0, stream, a, rows, 1);
-    }
-    const int vpt = nv <= 1024 ? 1 : nv <= 2048 ? 2 : 8;
-    const int warps = (nv + 32 * vpt - 1) / (32 * vpt);
-    const dim3 grid((unsigned)rows), block(warps * 32);
-    if (vpt == 1) return launch_pdl(rmsnorm_vec_kernel<1>, grid, block, 0, stream, a, rows, warps);
-    if (vpt == 2) return launch_pdl(rmsnorm_vec_kernel<2>, grid, block, 0, stream, a, rows, warps);
-    return launch_pdl(rmsnorm_vec_kernel<8>, grid, block, 0, stream, a, rows, warps);
+    const int64_t rows = mma ? mx_padded_rows(M) : M;
+    return K % 8 != 0 ? launch_vec<true>(a, rows, (int)(K + 14) / 8, stream) : launch_vec<false>(a, rows, (int)(K / 8), stream);
 }
 
 }  // namespace w4

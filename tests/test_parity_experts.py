@@ -268,8 +268,8 @@ def test_refusals(w4, bad):
     assert call(w4, **bad) == w4.W4_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("big", [dict(N=1 << 29), dict(P=(1 << 23) + 1, ws=FAKE, wbytes=1 << 40),
-                                 dict(R=1 << 31, order=FAKE)])
+@pytest.mark.parametrize("big", [dict(N=1 << 29, ws=FAKE, wbytes=1 << 40), dict(P=(1 << 23) + 1, ws=FAKE, wbytes=1 << 40),
+                                 dict(R=1 << 31, order=FAKE, ws=FAKE, wbytes=1 << 40)])
 def test_unsupported(w4, big):
     assert call(w4, **big) == w4.W4_ERR_UNSUPPORTED
 
