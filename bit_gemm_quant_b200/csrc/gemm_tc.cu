@@ -44,10 +44,7 @@
 // the last CTA of a tile (found with an atomic counter) sums the partials in
 // split order, writes Y and re-zeroes the counter.
 #include "common.cuh"
-#include "experts.cuh"
-#include "tc_ptx.cuh"
-
-#include <cuda.h>
+#include "tc_pipe.cuh"
 
 namespace w4 {
 
@@ -55,129 +52,19 @@ static __device__ int g_device_error;
 
 namespace {
 
-constexpr int kThreads = 320;
-constexpr int kKB = 64;                      // k per block (one 128-byte swizzle row of bf16)
-
-enum : int {
-    kErrWaitTma = 0x101, kErrWaitFullA = 0x102, kErrWaitEmptyTma = 0x103, kErrWaitEmptyDeq = 0x104,
-    kErrWaitDone = 0x105, kErrDrain = 0x106
-};
-
-// ---------------------------------------------------------------- PTX ----
-// Wait for the phase of `bar` with the given parity.  Gives up (returns false)
-// when the CTA's abort flag is raised or after `limit` ns, in which case it
-// records `code` and raises the abort flag.
-__device__ __noinline__ bool wait_bounded(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int code,
-                                         uint64_t limit)
-{
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (true) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (globaltimer() - t0 > limit) {
-            *abort_flag = 1;
-            atomicCAS(&g_device_error, 0, code);
-            return false;
-        }
-    }
-}
-
-// Drain wait: ignores the abort flag, bounded in time only.
-__device__ __noinline__ bool wait_drain(uint64_t *bar, uint32_t parity)
-{
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity)) {
-        if (globaltimer() - t0 > kDefaultWaitNs) {
-            atomicCAS(&g_device_error, 0, kErrDrain);
-            return false;
-        }
-    }
-    return true;
-}
-
-// Bounded wait until both barriers have completed the phase with the given
-// parity; each round tests both at once (their latencies overlap).
-__device__ __noinline__ bool wait_pair_bounded(uint64_t *a, uint64_t *b, uint32_t parity, volatile int *abort_flag,
-                                              uint64_t limit)
-{
-    const uint64_t t0 = globaltimer();
-    while (true) {
-        const bool ra = mbar_test(a, parity), rb = mbar_test(b, parity);
-        if (ra && rb) return true;
-        if (*abort_flag) return false;
-        if (globaltimer() - t0 > limit) {
-            *abort_flag = 1;
-            atomicCAS(&g_device_error, 0, kErrWaitFullA);
-            return false;
-        }
-    }
-}
-
-// One k-block (four 128 x BN x 16 MMAs, A from tensor memory at a_tmem, B
-// from the SW128 descriptor bdesc, accumulate unless acc0 == 0 for the first)
-// and its commit to `empty`, with non-blocking tests of the next k-block's
-// barriers issued first; returns whether both were complete.
-__device__ __forceinline__ bool mma_kblock_test_next(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                                     uint32_t acc0, uint64_t *empty, uint64_t *next_a,
-                                                     uint64_t *next_b, uint32_t next_parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred pa, pb, p0, p1;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 pa, [%1], %3;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 pb, [%2], %3;\n\t"
-        "setp.ne.b32 p0, %8, 0;\n\t"
-        "setp.eq.b32 p1, %8, %8;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%4], [%5], %6, %7, p0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%4], [%9], %10, %7, p1;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%4], [%11], %12, %7, p1;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%4], [%13], %14, %7, p1;\n\t"
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%15];\n\t"
-        "and.pred pa, pa, pb;\n\t"
-        "selp.u32 %0, 1, 0, pa;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(next_a)), "r"(smem_u32(next_b)), "r"(next_parity), "r"(d_tmem), "r"(a_tmem), "l"(bdesc),
-          "r"(idesc), "r"(acc0), "r"(a_tmem + 8), "l"(bdesc + 2), "r"(a_tmem + 16), "l"(bdesc + 4), "r"(a_tmem + 24),
-          "l"(bdesc + 6), "r"(smem_u32(empty))
-        : "memory");
-    return ok != 0;
-}
-
-template <int BN>
-struct TcCfg {
-    static constexpr int kCols = (BN <= 128) ? 256 : 512;               // tensor-memory allocation
-    // pipeline depth: as many 32-column A stages as fit beside the accumulator, at most 6 (even)
-    static constexpr int kStages = ((kCols - BN) / 32 >= 6) ? 6 : 4;
-    static constexpr int kACol0 = BN;                                   // A stages follow the BN fp32 accumulator columns
-    static constexpr int kBBytes = BN * 128;                            // activation box bytes
-    static constexpr int kCodeBytes = 128 * 32;                         // codes box: 128 channels x 64 k
-    static constexpr int kStageBytes = kBBytes + kCodeBytes;            // a multiple of 1024
-    static_assert(kACol0 + kStages * 32 <= kCols, "tensor memory overflow");
-    static constexpr int kMinBlocks = (BN == 256) ? 1 : 2;
-    // kind::f16, fp32 D, bf16 A and B, both K-major, N = BN, M = 128
-    static constexpr uint32_t kIdesc =
-        (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-};
-
 // Scales and zero-points of one channel's two 32-weight halves of a k-block.
 struct SlotData {
     unsigned short s0, s1;
     uint32_t z0, z1;
 };
 
-// With EXP the product is w4a16_experts_gemm's: CTA (x, y) owns channels
-// 128 x .. of one expert and up to BN of that expert's rows (unit y of the
-// plan).  N and the channels are per expert, the arrays of the E weights follow
-// one another, and X holds the sorted rows.  A box's rows past the unit's are
-// other rows of X, whose accumulator columns are never stored.
-template <int BN, bool EXP>
+template <int BN>
 __global__ void __launch_bounds__(kThreads, TcCfg<BN>::kMinBlocks)
 gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_q,
                const __grid_constant__ CUtensorMap tmap_y, int y_tma, int M, int N, int K, int group_log2, int asym,
                const uint4 *__restrict__ qweight, const unsigned short *__restrict__ scales,
                const uint32_t *__restrict__ qzeros, void *__restrict__ Y, int y_f32, float *__restrict__ partial,
-               unsigned *__restrict__ counters, int splits, int kb_per_split, uint64_t wait_ns, ExpertPlan plan)
+               unsigned *__restrict__ counters, int splits, int kb_per_split, uint64_t wait_ns)
 {
     using C = TcCfg<BN>;
     constexpr int kStages = C::kStages;
@@ -197,18 +84,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     const uint64_t limit = wait_limit_of(wait_ns);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n0 = blockIdx.x * 128, split = blockIdx.z;
-    int m0 = blockIdx.y * BN, q0 = n0;                                // first row of Y, first row of the code map
-    if (EXP) {
-        pdl_wait();                                                    // the plan is there
-        pdl_launch_dependents();
-        const ExpertUnit unit = find_unit(plan, blockIdx.y, BN);
-        if (unit.rows == 0) return;                                    // (every warp finds the same)
-        m0 = unit.row0;
-        M = m0 + unit.rows;
-        q0 = unit.expert * N + n0;
-        y_tma = y_tma && unit.rows == BN;                              // a whole tile, no other expert's rows
-    }
+    const int n0 = blockIdx.x * 128, m0 = blockIdx.y * BN, split = blockIdx.z;
     const int KQ = K >> 5;                                            // 16-byte code chunks per channel
     const int kb_total = (K + kKB - 1) / kKB;
     const int kb_begin = split * kb_per_split;
@@ -232,10 +108,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    if (!EXP) {
-        pdl_wait();                                                    // the previous kernel's writes are visible
-        pdl_launch_dependents();
-    }
+    pdl_wait();                                                       // the previous kernel's writes are visible
+    pdl_launch_dependents();
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer --
@@ -246,16 +120,16 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
             for (int i = 0; i < nkb; ++i) {
                 const int s = i % kStages;
                 const uint32_t ph = (i / kStages) & 1;
-                if (!mbar_try_wait(&empty[s], ph ^ 1) && !wait_bounded(&empty[s], ph ^ 1, abort_flag, kErrWaitEmptyTma, limit))
+                if (!mbar_try_wait(&empty[s], ph ^ 1) && !wait_bounded(&empty[s], ph ^ 1, abort_flag, &g_device_error, kErrWaitEmptyTma, limit))
                     break;
                 mbar_arrive_expect_tx(&full_b[s], C::kStageBytes);
                 tma_load_2d(sB + s * C::kStageBytes, &tmap_x, &full_b[s], (kb_begin + i) * kKB, m0);
-                tma_load_2d(sB + s * C::kStageBytes + C::kBBytes, &tmap_q, &full_b[s], (kb_begin + i) * 8, q0);
+                tma_load_2d(sB + s * C::kStageBytes + C::kBBytes, &tmap_q, &full_b[s], (kb_begin + i) * 8, n0);
                 ++issued;
             }
             // drain: every issued copy must have landed before the CTA may exit
             for (int i = max(0, issued - kStages); i < issued; ++i)
-                wait_drain(&full_b[i % kStages], (i / kStages) & 1);
+                wait_drain(&full_b[i % kStages], (i / kStages) & 1, &g_device_error);
         }
     } else if (warp == 1) {
         // ------------------------------------------------- MMA issuer ---
@@ -278,7 +152,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 for (int st = 0; st < kStages; ++st) {
                     const int i = i0 + st;
                     if (i >= nkb) break;
-                    if (!ready) ready = wait_pair_bounded(&full_a[st], &full_b[st], ph, abort_flag, limit);
+                    if (!ready) ready = wait_pair_bounded(&full_a[st], &full_b[st], ph, abort_flag, &g_device_error, limit);
                     if (!ready) {
                         stop = true;
                         break;
@@ -295,7 +169,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 }
             }
             mma_commit(done);
-            wait_drain(done, 0);   // no MMA may still be running when tensor memory is freed
+            wait_drain(done, 0, &g_device_error);   // no MMA may still be running when tensor memory is freed
         }
         __syncwarp();
     } else {
@@ -305,8 +179,8 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         const int r = 32 * q + lane;
         const int n = n0 + r;
         const bool okn = n < N;
-        const unsigned short *srow = scales + (size_t)(okn ? q0 + r : 0) * NG;
-        const uint32_t *zrow = qzeros + (size_t)(okn ? q0 + r : 0) * ZW;
+        const unsigned short *srow = scales + (size_t)(okn ? n : 0) * NG;
+        const uint32_t *zrow = qzeros + (size_t)(okn ? n : 0) * ZW;
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * q) << 16);
 
         // the codes arrive with the activations (TMA, full_b); only the scales
@@ -352,7 +226,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
                 uint64_t *fb = (i == h && stalls_first_wait(wait_ns)) ? stall : &full_b[s];
                 const uint32_t fph = fb == stall ? 0u : ph;
                 if (!__all_sync(0xffffffffu, mbar_try_wait(fb, fph) ||
-                                                 wait_bounded(fb, fph, abort_flag, kErrWaitEmptyDeq, limit))) {
+                                                 wait_bounded(fb, fph, abort_flag, &g_device_error, kErrWaitEmptyDeq, limit))) {
                     ok = false;
                     break;
                 }
@@ -388,7 +262,7 @@ gemm_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
         }
 
         // ---- epilogue: accumulator -> Y (or fp32 partials) ----
-        const bool have = __all_sync(0xffffffffu, ok && wait_bounded(done, 0, abort_flag, kErrWaitDone, limit));
+        const bool have = __all_sync(0xffffffffu, ok && wait_bounded(done, 0, abort_flag, &g_device_error, kErrWaitDone, limit));
         tc_fence_after();
         constexpr int HALF = BN / 2;                  // columns per warp of a lane quarter
         const int cbeg = h * HALF;
@@ -538,7 +412,7 @@ cudaError_t launch_bn(const CUtensorMap &map, const CUtensorMap &qmap, const CUt
     if (C::kMinBlocks == 2 && smem < 80 * 1024) smem = 80 * 1024;   // at most 2 CTAs share an SM's tensor memory
     static std::atomic<bool> attr_done[kMaxDevices];   // the attribute is per device
     {
-        const cudaError_t e = set_smem_attr(gemm_tc_kernel<BN, false>, (int)smem, attr_done);
+        const cudaError_t e = set_smem_attr(gemm_tc_kernel<BN>, (int)smem, attr_done);
         if (e != cudaSuccess) return e;
     }
     float *partial = nullptr;
@@ -549,26 +423,9 @@ cudaError_t launch_bn(const CUtensorMap &map, const CUtensorMap &qmap, const CUt
         counters = (unsigned *)((uint8_t *)ws + ((part + 255) & ~(size_t)255));
     }
     dim3 grid(p.n_tiles, p.m_tiles, p.splits);
-    return launch_pdl(gemm_tc_kernel<BN, false>, grid, dim3(kThreads), smem, stream, map, qmap, ymap, y_tma, M, N, K, glog2,
+    return launch_pdl(gemm_tc_kernel<BN>, grid, dim3(kThreads), smem, stream, map, qmap, ymap, y_tma, M, N, K, glog2,
                       asym, (const uint4 *)qweight, (const unsigned short *)scales, qzeros, Y, y_f32,
-                      partial, counters, p.splits, p.kb_per_split, wait_limit_ns(), ExpertPlan{});
-}
-
-template <int BN>
-cudaError_t launch_experts_bn(const CUtensorMap &map, const CUtensorMap &qmap, const CUtensorMap &ymap, int y_tma,
-                              const ExpertPlan &plan, int N, int K, int glog2, int asym, const uint32_t *qweight,
-                              const void *scales, const uint32_t *qzeros, void *Y, cudaStream_t stream)
-{
-    using C = TcCfg<BN>;
-    size_t smem = 1024 + C::kStages * C::kStageBytes + 256;
-    if (C::kMinBlocks == 2 && smem < 80 * 1024) smem = 80 * 1024;   // at most 2 CTAs share an SM's tensor memory
-    static std::atomic<bool> attr_done[kMaxDevices];
-    const cudaError_t e = set_smem_attr(gemm_tc_kernel<BN, true>, (int)smem, attr_done);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((N + 127) / 128), (unsigned)max_units(plan.P, plan.E, BN));
-    return launch_pdl(gemm_tc_kernel<BN, true>, grid, dim3(kThreads), smem, stream, map, qmap, ymap, y_tma, 0, N, K,
-                      glog2, asym, (const uint4 *)qweight, (const unsigned short *)scales, qzeros, Y, 0,
-                      (float *)nullptr, (unsigned *)nullptr, 1, (K + kKB - 1) / kKB, wait_limit_ns(), plan);
+                      partial, counters, p.splits, p.kb_per_split, wait_limit_ns());
 }
 
 }  // namespace
@@ -634,80 +491,6 @@ cudaError_t launch_gemm_tc(const void *X, int64_t M, int64_t N, int64_t K, const
     case 64: return launch_bn<64>(map, qmap, ymap, y_tma, p, (int)M, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, y_f32 ? 1 : 0, ws, stream);
     case 128: return launch_bn<128>(map, qmap, ymap, y_tma, p, (int)M, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, y_f32 ? 1 : 0, ws, stream);
     default: return launch_bn<256>(map, qmap, ymap, y_tma, p, (int)M, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, y_f32 ? 1 : 0, ws, stream);
-    }
-}
-
-// The rows of X in sorted order: dst[i] = X[order[i] / top_k] for i < offsets[E],
-// 16 bytes a thread and step.  The product's CTAs read each row N / 128 times, in
-// boxes of BN rows; TMA's four-row gather took about 50 cycles an instruction and
-// left the product at 232 TFLOP/s (8192 tokens, 2 of 8 experts of [14336, 4096]),
-// so the rows are moved once instead: 4 K bytes a row.
-__global__ void __launch_bounds__(256) sort_rows_kernel(const uint4 *X, ExpertPlan plan, int vecs, uint4 *dst)
-{
-    pdl_wait();
-    pdl_launch_dependents();
-    const int rows = min(max(plan.offsets[plan.E], 0), plan.P);
-    const int64_t total = (int64_t)rows * vecs;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int row = (int)(i / vecs), v = (int)(i - (int64_t)row * vecs);
-        dst[i] = X[(int64_t)expert_x_row(plan, row) * vecs + v];
-    }
-}
-
-size_t experts_tc_workspace_bytes(int64_t P, int64_t K) { return (size_t)P * K * 2; }
-
-cudaError_t launch_experts_tc(const void *X, ExpertPlan plan, int64_t N, int64_t K, const uint32_t *qweight,
-                              const void *scales, const uint32_t *qzeros, int group, int mode, void *Y, void *ws,
-                              cudaStream_t stream)
-{
-    EncodeTiledFn enc = encode_fn();
-    if (!enc) return cudaErrorNotSupported;
-    if (plan.order) {
-        const int64_t want = (plan.P * (K / 8) + 255) / 256;
-        const unsigned grid = (unsigned)(want < (int64_t)kNumSMs * 16 ? want : (int64_t)kNumSMs * 16);
-        const cudaError_t e = launch_pdl(sort_rows_kernel, dim3(grid), dim3(256), 0, stream, (const uint4 *)X, plan,
-                                         (int)(K / 8), (uint4 *)ws);
-        if (e != cudaSuccess) return e;
-        X = ws;
-        plan.order = nullptr;
-    }
-    const int64_t rows = plan.P / plan.E;
-    const int BN = rows <= 20 ? 32 : rows <= 48 ? 64 : rows <= 400 ? 128 : 256;
-    CUtensorMap map, qmap, ymap;
-    const cuuint64_t gdim[2] = {(cuuint64_t)K, (cuuint64_t)plan.P};
-    const cuuint64_t gstride[1] = {(cuuint64_t)K * 2};
-    const cuuint32_t box[2] = {(cuuint32_t)kKB, (cuuint32_t)BN};
-    const cuuint32_t estride[2] = {1, 1};
-    if (enc(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(X), gdim, gstride, box, estride,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    const cuuint64_t qdim[2] = {(cuuint64_t)(K / 8), (cuuint64_t)(plan.E * N)};
-    const cuuint64_t qstride[1] = {(cuuint64_t)K / 2};
-    const cuuint32_t qbox[2] = {8u, 128u};
-    if (enc(&qmap, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint32_t *>(qweight), qdim, qstride, qbox, estride,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
-    ymap = map;
-    int y_tma = 0;
-    if (((uintptr_t)Y % 16) == 0 && (N * 2) % 16 == 0) {
-        const cuuint64_t ydim[2] = {(cuuint64_t)N, (cuuint64_t)plan.P};
-        const cuuint64_t ystride[1] = {(cuuint64_t)N * 2};
-        const cuuint32_t ybox[2] = {128u, (cuuint32_t)BN};
-        if (enc(&ymap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, Y, ydim, ystride, ybox, estride,
-                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-            return cudaErrorInvalidValue;
-        y_tma = 1;
-    }
-    const int glog2 = group == 32 ? 5 : group == 64 ? 6 : 7;
-    const int asym = mode == W4_ASYM;
-    switch (BN) {
-    case 32: return launch_experts_bn<32>(map, qmap, ymap, y_tma, plan, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, stream);
-    case 64: return launch_experts_bn<64>(map, qmap, ymap, y_tma, plan, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, stream);
-    case 128: return launch_experts_bn<128>(map, qmap, ymap, y_tma, plan, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, stream);
-    default: return launch_experts_bn<256>(map, qmap, ymap, y_tma, plan, (int)N, (int)K, glog2, asym, qweight, scales, qzeros, Y, stream);
     }
 }
 
