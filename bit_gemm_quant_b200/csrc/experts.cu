@@ -169,10 +169,12 @@ experts_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *
     pdl_wait();
     pdl_launch_dependents();
 
-    // X into L2, a slice by every CTA, before the codes fill the queues to memory
-    if (threadIdx.x == 32) {
-        const size_t part = ((size_t)plan.R * K + gridDim.x - 1) / gridDim.x, from = part * blockIdx.x;
-        if (from < (size_t)plan.R * K) prefetch_l2(X + from, min(part, (size_t)plan.R * K - from) * 2);
+    // the rows of X into L2, a slice by every CTA, before the codes fill the queues to memory (unless X has
+    // more rows than the plan: most of it is somebody else's then)
+    if (threadIdx.x == 32 && (!plan.order || plan.R <= plan.P)) {
+        const size_t all = (size_t)min(plan.R, plan.P) * K, part = (all + gridDim.x - 1) / gridDim.x;
+        const size_t from = part * blockIdx.x;
+        if (from < all) prefetch_l2(X + from, min(part, all - from) * 2);
     }
     // the plan: offsets, then the units' running count by the first warp
     for (int e = threadIdx.x; e <= plan.E; e += kNW * 32) off[e] = min(max(plan.offsets[e], 0), plan.P);

@@ -159,6 +159,69 @@ def test_a_wrong_plan_stays_inside_the_arrays(w4, T):
     assert (out[-1] == 777).all() and w4.w4_device_error() == 0
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,lo,hi", [(2, 0x401, 0x402), (300, 0x101, 0x106)], ids=["streaming", "tensor_core"])
+def test_wait_runs_out_then_next_call_is_correct(w4, T, lo, hi):
+    """The failure path without a fault (test_failure_path.py): a wait that runs
+    out is reported, nothing hangs, and the next calls are right (a leaked
+    tensor-memory allocation would stall them)."""
+    from test_failure_path import run_with_short_limit
+    layer = Layer(w4, 8, 520, 1024, 128, ASYM, seed=10)
+    ids = random_ids(T, 8, 2, 5)
+    offsets, order = plan_of(ids, 8)
+    import torch
+    X = dev_bf16(synth.activations(2, T, 1024))
+    off, order = torch.from_numpy(offsets).cuda(), torch.from_numpy(order).cuda()
+    for _ in range(3):
+        code = run_with_short_limit(w4, lambda: layer(w4, X, off, order=order, top_k=2))
+        assert lo <= code <= hi, hex(code)
+        check(w4, layer, ids, True)
+
+
+@pytest.mark.gpu
+def test_calls_at_once(w4):
+    """Layers on two streams at the same time give the bits that each gives alone."""
+    import torch
+    layer = Layer(w4, 8, 520, 1024, 64, ASYM, seed=11)
+    jobs = []
+    for T in (3, 200, 5, 500):
+        ids = random_ids(T, 8, 2, T)
+        offsets, order = (torch.from_numpy(a).cuda() for a in plan_of(ids, 8))
+        X = dev_bf16(synth.activations(T, T, 1024))
+        jobs.append((X, offsets, order, layer(w4, X, offsets, order=order, top_k=2)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [[layer(w4, X, off, order=order, top_k=2, stream=streams[i % 2]) for i, (X, off, order, _) in enumerate(jobs)]
+               for _ in range(4)]
+        torch.cuda.synchronize()
+        for r in got:
+            for y, job in zip(r, jobs):
+                assert torch.equal(y, job[3])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 64])
+def test_arrays_past_32_bits(w4, T):
+    """Codes of more than 2^32 bytes: the last expert's weights are at their end."""
+    import torch
+    E, N, K, g = 9, 131072, 8192, 128
+    q = torch.zeros(E, N, K // 8, dtype=torch.int32, device="cuda")
+    s = torch.zeros(E, N, K // g, dtype=torch.float16, device="cuda")
+    packed = w4.quant_pack(dev_bf16(synth.weights(77, 200, K, 0.02)), g, SYM)
+    q[-1, -200:], s[-1, -200:] = packed[0], packed[1]
+    X = dev_bf16(synth.activations(78, T, K))
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[-1] = T
+    Y = w4.experts_gemm(X, q, s, None, g, SYM, offsets)
+    want = w4.gemm(X, packed[0], packed[1], None, g, SYM).double()
+    # two sums of the same terms in fp32, in another order, each rounded to bf16: two half steps of 2^-8
+    # and K 2^-22 of the terms' magnitudes (parity.py), those below 2^5 of the result's scale here
+    diff = (Y[:, -200:].double() - want).norm() / want.norm()
+    assert diff <= 2 * 2.0 ** -8 + 2 * K * 2.0 ** -22 * 2 ** 5
+    assert (Y[:, :-200] == 0).all()
+
+
 # ------------------------------------------------- the operators together --
 
 def forward(w4, x, r, gamma, gate, up, down, k, bias):

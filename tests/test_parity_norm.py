@@ -206,6 +206,23 @@ def test_unaligned_pointers(w4):
     between(f64(host_u16(H)), h, bf16, "H")
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("K", [8192, 8191])
+def test_rows_past_32_bits(w4, K):
+    """More than 2^31 elements: the last rows are as they are alone."""
+    import torch
+    M = 2 ** 31 // K + 50
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    tail, _, gamma = inputs(40, K, 41, residual=False)
+    x[-40:] = dev(tail)
+    x[0] = dev(tail)[0]
+    Y, _ = w4.rmsnorm(x, dev(gamma), EPS)
+    Z, _ = w4.rmsnorm(x[-40:].clone(), dev(gamma), EPS)
+    assert (Y[1:-40] == 0).all() and torch.equal(Y[0], Z[0])
+    _, y = reference(tail, None, gamma)
+    between(f64(host_u16(Y[-40:])), y, bf16, "Y")
+
+
 # ------------------------------------------------------------- refusals --
 
 FAKE = 1 << 20

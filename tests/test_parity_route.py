@@ -30,7 +30,8 @@ def choose(x, k, sigmoid=False, bias=None, groups=1, keep=1, group_top=1, renorm
         live = ~np.isneginf(x[t])
         score = np.zeros(E)
         if sigmoid:
-            score[live] = 1 / (1 + np.exp(-x[t][live]))
+            with np.errstate(over="ignore"):
+                score[live] = 1 / (1 + np.exp(-x[t][live]))
         elif live.any():
             score[live] = np.exp(x[t][live] - x[t][live].max())
             score /= score.sum()
@@ -249,6 +250,21 @@ def test_combine_in_place_and_unwritten_rows(w4, N):
     assert torch.isfinite(want).all() and torch.equal(want[2], A[2])
     got = w4.combine(Y, pos, w, add=A, out=A)
     assert got.data_ptr() == A.data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [8192, 8191])
+def test_combine_past_32_bits(w4, N):
+    import torch
+    P, k = 2 ** 31 // N + 40, 2
+    Y = torch.zeros(P, N, dtype=torch.bfloat16, device="cuda")
+    Y[-1] = 1.0
+    Y[0] = 2.0
+    pos = torch.full((P, k), -1, dtype=torch.int32, device="cuda")
+    pos[-1, 0], pos[-1, 1], pos[0, 1] = P - 1, 0, P - 1
+    w = torch.full((P, k), 0.5, device="cuda")
+    out = w4.combine(Y, pos, w)
+    assert (out[-1] == 1.5).all() and (out[0] == 0.5).all() and (out[1:-1] == 0).all()
 
 
 # ------------------------------------------------------------- refusals --
