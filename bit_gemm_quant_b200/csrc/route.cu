@@ -21,17 +21,22 @@
 // experts 0, below every number); its maximum over the warp takes two 32-bit
 // reductions (three for fp64): the key, then the lowest index that has it.
 //
-// The plan needs no scan across CTAs: the CTA of expert e reads all ids, counts
-// those below e (where its rows begin) and lists its own pairs in order.  Up to
+// The plan of up to kPlanMany pairs needs no scan across CTAs: the CTA of expert e
+// reads all ids, counts those below e (where its rows begin) and lists its own
+// pairs in order; more pairs are counted and placed by one cluster.  Up to
 // kFusedPairs pairs of kFusedWarps tokens the one CTA that chooses also makes the
 // plan, each thread ranking one pair against all others in shared memory: one
 // launch in place of two.  (57 tokens that way took 11.9 us, against 5.2 in two.)
 // What bounds it: latency.  8192 tokens, 8 of 128 experts (4.7 MB, 0.8 us of HBM)
-// take 20.7 us; with fp64 scores for the choice, and each thread of the plan
-// reading a run of ids of its own, 88.
+// take 18 us, 8.5 of them the choice; one token, 8 of 256 experts in 8 groups,
+// sigmoid and bias, 7.8 us, half of it the fp64 scores.
 #include "common.cuh"
 
+#include <cooperative_groups.h>
+
 #include <type_traits>
+
+namespace cg = cooperative_groups;
 
 namespace w4 {
 namespace {
@@ -47,6 +52,7 @@ struct RouteArgs {
     int64_t T;
     int E, k, f32, sigmoid, groups, keep, group_top, renorm;
     float scale;
+    int size, lanes_log2;                                 // of a group: its experts, and log2 of the lanes that look through it
 };
 
 // Floating values as unsigned integers of the same order; 0 stands below all of
@@ -79,132 +85,180 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
-// The warp's largest key and the lowest index that has it.
-__device__ __forceinline__ int warp_best(uint32_t key, int idx, uint32_t &best)
+// The double behind a key above 1.
+__device__ __forceinline__ double key_value(uint64_t k)
 {
-    best = __reduce_max_sync(kFull, key);
-    return (int)__reduce_min_sync(kFull, key == best ? (unsigned)idx : kFull);
+    return __longlong_as_double((long long)((k >> 63) ? k & ~(1ull << 63) : ~k));
 }
 
-__device__ __forceinline__ int warp_best(uint64_t key, int idx, uint64_t &best)
+// The lowest index among the lanes with the warp's largest key, -1 if every key
+// is 0.  Mostly one lane alone has the largest (high) word.
+__device__ __forceinline__ int warp_best(uint32_t key, int idx)
+{
+    const uint32_t best = __reduce_max_sync(kFull, key);
+    const unsigned who = __ballot_sync(kFull, key == best);
+    if ((who & (who - 1)) == 0) return __shfl_sync(kFull, key ? idx : -1, __ffs(who) - 1);
+    return best ? (int)__reduce_min_sync(kFull, key == best ? (unsigned)idx : kFull) : -1;
+}
+
+__device__ __forceinline__ int warp_best(uint64_t key, int idx)
 {
     const uint32_t hi = (uint32_t)(key >> 32);
     const uint32_t mh = __reduce_max_sync(kFull, hi);
+    const unsigned who = __ballot_sync(kFull, hi == mh);
+    if ((who & (who - 1)) == 0) return __shfl_sync(kFull, key ? idx : -1, __ffs(who) - 1);
     const uint32_t ml = __reduce_max_sync(kFull, hi == mh ? (uint32_t)key : 0u);
-    best = ((uint64_t)mh << 32) | ml;
-    return (int)__reduce_min_sync(kFull, key == best ? (unsigned)idx : kFull);
+    const uint64_t best = ((uint64_t)mh << 32) | ml;
+    return best ? (int)__reduce_min_sync(kFull, key == best ? (unsigned)idx : kFull) : -1;
 }
 
-// What a group is worth, and how the larger of two is found: the keys
-// themselves (SIMPLE), or fp64 choices that are summed.
+// What a group with the best keys m1 >= m2 is worth, as a key.
+__device__ __forceinline__ uint32_t group_key(uint32_t m1, uint32_t, int) { return m1; }
+__device__ __forceinline__ uint64_t group_key(uint64_t m1, uint64_t m2, int top)
+{
+    return top == 2 && m2 > 1 ? order_key(key_value(m1) + key_value(m2)) : m1;
+}
+
 template <bool SIMPLE>
-struct Choice;
-template <>
-struct Choice<true> {
-    typedef uint32_t Key, Value;
-    static __device__ __forceinline__ Value none() { return 0u; }
-    static __device__ __forceinline__ Value larger(Value a, Value b) { return max(a, b); }
-    static __device__ __forceinline__ Value smaller(Value a, Value b) { return min(a, b); }
-    static __device__ __forceinline__ Key group(Value m1, Value, int) { return m1; }
+struct KeyOf {
+    typedef uint64_t type;
 };
 template <>
-struct Choice<false> {
-    typedef uint64_t Key;
-    typedef double Value;
-    static __device__ __forceinline__ Value none() { return -INFINITY; }
-    static __device__ __forceinline__ Value larger(Value a, Value b) { return fmax(a, b); }
-    static __device__ __forceinline__ Value smaller(Value a, Value b) { return fmin(a, b); }
-    static __device__ __forceinline__ Key group(Value m1, Value m2, int top)
-    {
-        return order_key(top == 2 && m2 > -INFINITY ? m1 + m2 : m1);
-    }
+struct KeyOf<true> {
+    typedef uint32_t type;
 };
 
-__device__ __forceinline__ double sigmoid64(double x) { return 1.0 / (1.0 + exp(-x)); }
+// exp(v) for v <= 0, without a branch, so that a lane's experts run side by side
+// (the library's exp and division one after the other took 750 clocks an
+// expert): v = n ln 2 + r with ln 2 in two parts (Cody and Waite), |r| <= 0.35,
+// and the Taylor polynomial of degree 14 (its remainder is below 2^-63 e^r).
+// Below -708, where 2^n leaves the normal range, 0.
+__device__ __forceinline__ double exp_neg(double v)
+{
+    constexpr double kLn2 = 0.693147180559945309417232121458176568;
+    constexpr double kLn2Hi = 0x1.62e42feep-1;       // its leading 32 bits: n times this is exact
+    constexpr double kLn2Lo = 1.9082149292705877e-10;   // the rest
+    const double a = v < -708.0 ? -708.0 : v;        // (keeps a NaN)
+    const double n = rint(a * (1.0 / kLn2));
+    const double r = fma(-n, kLn2Lo, fma(-n, kLn2Hi, a));
+    double p = 1.0 / 87178291200.0;                  // 1 / 14!
+    p = fma(p, r, 1.0 / 6227020800.0);
+    p = fma(p, r, 1.0 / 479001600.0);
+    p = fma(p, r, 1.0 / 39916800.0);
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    const double two_n = __hiloint2double((1023 + (int)n) << 20, 0);
+    return v < -708.0 ? 0.0 : p * two_n;
+}
 
-// The choice for token t by one warp; S >= E / 32 experts per lane.  `sh`: E + 64
-// 8-byte words of this warp's shared memory (groups only).  Returns the id that
-// this lane's place j = lane got, and writes ids and weights.
+// 1 / d for 1 <= d <= 2: an approximate fp32 reciprocal (2^-22) and two Newton steps.
+__device__ __forceinline__ double reciprocal(double d)
+{
+    float f;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"((float)d));
+    double y = (double)f;
+    y = fma(y, fma(-d, y, 1.0), y);
+    return fma(y, fma(-d, y, 1.0), y);
+}
+
+__device__ __forceinline__ double sigmoid64(double x)
+{
+    const double e = exp_neg(-fabs(x)), inv = reciprocal(1.0 + e);
+    return x < 0.0 ? e * inv : inv;
+}
+
+__device__ __forceinline__ float logit(const RouteArgs &a, int64_t i)
+{
+    return a.f32 ? __ldg((const float *)a.logits + i) : __bfloat162float(__ldg((const __nv_bfloat16 *)a.logits + i));
+}
+
+// The choice for token t by one warp; S >= E / 32 experts per lane, a power of
+// two.  `sh`: E + 64 8-byte words of this warp's shared memory (groups only).
+// Returns the id that this lane's place j = lane got, and writes ids and weights.
 template <int S, bool SIMPLE>
 __device__ __forceinline__ int choose(const RouteArgs &a, int64_t t, uint64_t *sh)
 {
-    typedef Choice<SIMPLE> Ch;
-    typedef typename Ch::Key Key;
-    typedef typename Ch::Value Value;
+    typedef typename KeyOf<SIMPLE>::type Key;
     const int lane = threadIdx.x & 31;
     float x[S];
     Key key[S];
-    double score[SIMPLE ? 1 : S];
     float top = -INFINITY;
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-        const int e = lane + 32 * s;
-        x[s] = -INFINITY;
-        if (e < a.E)
-            x[s] = a.f32 ? __ldg((const float *)a.logits + t * a.E + e)
-                         : __bfloat162float(__ldg((const __nv_bfloat16 *)a.logits + t * a.E + e));
+        x[s] = lane + 32 * s < a.E ? logit(a, t * a.E + lane + 32 * s) : -INFINITY;
         top = fmaxf(top, x[s]);
     }
-    double total = 1.0;                                   // the softmax's sum, where it is wanted
+    double total = 1.0;                                   // one over the softmax's sum, where it is wanted
+    double score[SIMPLE ? 1 : S];
     if (!a.sigmoid && (!SIMPLE || !a.renorm)) {
         top = warp_max(top);
         total = 0.0;
 #pragma unroll
         for (int s = 0; s < S; ++s) {
-            const double v = x[s] != -INFINITY ? exp((double)x[s] - (double)top) : 0.0;
+            const double v = x[s] != -INFINITY ? exp_neg((double)x[s] - (double)top) : 0.0;
             if (!SIMPLE) score[SIMPLE ? 0 : s] = v;
             total += v;
         }
         total = warp_sum(total);
-        total = total > 0.0 ? total : 1.0;
+        total = total > 0.0 ? 1.0 / total : 1.0;
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+            if (!SIMPLE) score[SIMPLE ? 0 : s] *= total;
+    }
+    if (!SIMPLE && a.sigmoid) {                           // (outside the loop below: side by side, no branch between)
+#pragma unroll
+        for (int s = 0; s < S; ++s) score[SIMPLE ? 0 : s] = sigmoid64((double)x[s]);
     }
 #pragma unroll
     for (int s = 0; s < S; ++s) {
         const int e = lane + 32 * s;
         if (SIMPLE) {
-            key[s] = order_key(x[s]);
-            if (a.groups > 1 && e < a.E) ((uint32_t *)sh)[e] = (uint32_t)key[s];
+            key[s] = (Key)order_key(x[s]);
         } else {
-            double &sc = score[SIMPLE ? 0 : s];
-            const bool live = x[s] != -INFINITY;          // (a NaN stays, and spoils its own token only)
-            sc = !live ? 0.0 : a.sigmoid ? sigmoid64((double)x[s]) : sc / total;
-            const double c = sc + (a.bias && e < a.E ? (double)__ldg(a.bias + e) : 0.0);
-            key[s] = live ? (Key)order_key(c) : (Key)0;
-            if (a.groups > 1 && e < a.E) ((double *)sh)[e] = live ? c : -INFINITY;
+            const double c = score[SIMPLE ? 0 : s] + (a.bias && e < a.E ? (double)__ldg(a.bias + e) : 0.0);
+            key[s] = x[s] != -INFINITY ? (Key)order_key(c) : (Key)0;   // (a NaN spoils its own token only)
         }
+        if (a.groups > 1 && e < a.E) ((Key *)sh)[e] = key[s];
     }
     if (a.groups > 1) {
         // a group's two best choices, by `per_group` lanes each
-        const int size = a.E / a.groups;
-        int per_group = 1;
-        while (per_group * 2 * a.groups <= 32) per_group *= 2;
+        const int size = a.size, per_group = 1 << a.lanes_log2;
         Key *gkey = (Key *)(sh + a.E);
-        const int sub = lane & (per_group - 1), first = lane / per_group;
+        const int sub = lane & (per_group - 1), first = lane >> a.lanes_log2;
         __syncwarp();
-        for (int g0 = 0; g0 < a.groups; g0 += 32 / per_group) {
+        for (int g0 = 0; g0 < a.groups; g0 += 32 >> a.lanes_log2) {
             const int g = g0 + first;
-            Value m1 = Ch::none(), m2 = Ch::none();
+            Key m1 = 0, m2 = 0;
             if (g < a.groups)
                 for (int i = sub; i < size; i += per_group) {
-                    const Value c = ((const Value *)sh)[g * size + i];
-                    m2 = Ch::larger(m2, Ch::smaller(m1, c));
-                    m1 = Ch::larger(m1, c);
+                    const Key c = ((const Key *)sh)[g * size + i];
+                    m2 = max(m2, min(m1, c));
+                    m1 = max(m1, c);
                 }
             for (int d = 1; d < per_group; d *= 2) {
-                const Value n1 = __shfl_xor_sync(kFull, m1, d), n2 = __shfl_xor_sync(kFull, m2, d);
-                m2 = Ch::larger(Ch::smaller(m1, n1), Ch::larger(m2, n2));
-                m1 = Ch::larger(m1, n1);
+                const Key n1 = __shfl_xor_sync(kFull, m1, d), n2 = __shfl_xor_sync(kFull, m2, d);
+                m2 = max(min(m1, n1), max(m2, n2));
+                m1 = max(m1, n1);
             }
-            if (sub == 0 && g < a.groups) gkey[g] = Ch::group(m1, m2, a.group_top);
+            if (sub == 0 && g < a.groups) gkey[g] = group_key(m1, m2, a.group_top);
         }
         __syncwarp();
+        const float per = 1.0f / (float)size;             // (e + 1/2) / size is at least 2^-11 from a whole number
         Key k0 = lane < a.groups ? gkey[lane] : 0, k1 = lane + 32 < a.groups ? gkey[lane + 32] : 0;
         uint64_t kept = 0;                                // the groups that stay, one bit each
         for (int i = 0; i < a.keep; ++i) {
-            Key best;
             const bool low = k0 >= k1;
-            const int g = warp_best(low ? k0 : k1, low ? lane : lane + 32, best);
-            if (best == 0) break;
+            const int g = warp_best(low ? k0 : k1, low ? lane : lane + 32);
+            if (g < 0) break;
             kept |= 1ull << g;
             if (g == lane) k0 = 0;
             if (g == lane + 32) k1 = 0;
@@ -212,44 +266,40 @@ __device__ __forceinline__ int choose(const RouteArgs &a, int64_t t, uint64_t *s
 #pragma unroll
         for (int s = 0; s < S; ++s) {
             const int e = lane + 32 * s;
-            if (e < a.E && !(kept >> (e / size) & 1)) key[s] = 0;
+            if (e < a.E && !(kept >> (int)(((float)e + 0.5f) * per) & 1)) key[s] = 0;
         }
         __syncwarp();                                     // the next token of this warp writes sh again
     }
     int id = -1;
-    float chosen = 0.f;                                   // SIMPLE: the chosen logit, else its score
-    double w = 0.0;
     for (int j = 0; j < a.k; ++j) {
-        Key mine = 0, best;
-        int at = 0;
-        float xb = 0.f;
-        double sb = 0.0;
+        // this lane's best, pairwise (equal keys: the lower slot)
+        Key m[S];
+        int at[S];
 #pragma unroll
-        for (int s = 0; s < S; ++s)
-            if (key[s] > mine) {
-                mine = key[s];
-                at = s;
-                if (SIMPLE) xb = x[s];
-                else sb = score[SIMPLE ? 0 : s];
-            }
-        const int e = warp_best(mine, lane + 32 * at, best);
-        if (best == 0) break;
-        if (SIMPLE) xb = __shfl_sync(kFull, xb, e & 31);
-        else sb = __shfl_sync(kFull, sb, e & 31);
-        if (lane == j) {
-            id = e;
-            chosen = xb;
-            w = sb;
+        for (int s = 0; s < S; ++s) {
+            m[s] = key[s];
+            at[s] = s;
         }
+#pragma unroll
+        for (int d = 1; d < S; d *= 2)
+#pragma unroll
+            for (int s = 0; s + d < S; s += 2 * d)
+                if (m[s + d] > m[s]) {
+                    m[s] = m[s + d];
+                    at[s] = at[s + d];
+                }
+        const int e = warp_best(m[0], lane + 32 * at[0]);
+        if (e < 0) break;
+        if (lane == j) id = e;
 #pragma unroll
         for (int s = 0; s < S; ++s)
             if (lane + 32 * s == e) key[s] = 0;
     }
-    if (SIMPLE) {
-        // (renormalised, a softmax needs no common sum: the largest chosen logit is place 0's)
-        const float ref = a.renorm ? __shfl_sync(kFull, chosen, 0) : top;
-        if (id >= 0) w = a.sigmoid ? sigmoid64((double)chosen) : exp((double)chosen - (double)ref) / total;
-    }
+    // the scores of the chosen, by the lane of each
+    const float xc = id >= 0 ? logit(a, t * a.E + id) : 0.f;
+    // (renormalised without other need of it, a softmax has no common sum: the largest chosen logit is place 0's)
+    const float ref = SIMPLE && a.renorm ? __shfl_sync(kFull, xc, 0) : top;
+    double w = id < 0 ? 0.0 : a.sigmoid ? sigmoid64((double)xc) : exp_neg((double)xc - (double)ref) * total;
     if (a.renorm) {
         const double sum = warp_sum(w);
         w = sum > 0.0 ? w / sum : 0.0;
@@ -361,6 +411,106 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int *ids, int P, int E
     }
 }
 
+// The plan of many pairs, by one cluster of kPlanCtas CTAs: CTA c has the c-th
+// contiguous part of the ids and warp w the w-th part of that, 32 at a time.
+// Every warp counts its pairs of each expert; the counts are summed over the
+// warps of a CTA and, through distributed shared memory, over the CTAs, which
+// with the sum over the lower experts gives the row of each warp's first pair of
+// each expert; then the ids are read again and placed, lanes with the same id
+// (found by a ballot for each bit of the id; the match instruction took 2000
+// clocks with 32 warps at it) in their order.  `sh`: kPlanWarps + 2 rows of E
+// counts.
+constexpr int kPlanCtas = 8, kPlanWarps = 32, kPlanMany = 32768;
+
+__global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanWarps * 32)
+plan_many_kernel(const int *ids, int P, int E, int id_bits, int *offsets, int *order, int *pos)
+{
+    extern __shared__ int sh[];
+    __shared__ int warp_total[32];
+    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int *mine = sh + warp * E;                            // this warp's counts, then rows
+    int *total = sh + kPlanWarps * E, *start = total + E; // this CTA's counts, and the first rows of its pairs
+    cg::cluster_group cluster = cg::this_cluster();
+    for (int i = threadIdx.x; i < kPlanWarps * E; i += blockDim.x) sh[i] = 0;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int part = (P + kPlanCtas * kPlanWarps - 1) / (kPlanCtas * kPlanWarps);
+    const int64_t from = (int64_t)(c * kPlanWarps + warp) * part;
+    const int lo = (int)(from < P ? from : P), hi = min(P, lo + part);
+    __syncthreads();
+    constexpr int kBatch = 8;                             // loads in flight
+    int id[kBatch];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) id[i] = p0 + 32 * i + lane < hi ? __ldg(ids + p0 + 32 * i + lane) : -1;
+    };
+    for (int p0 = lo; p0 < hi; p0 += 32 * kBatch) {
+        load(p0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (id[i] >= 0) atomicAdd(mine + id[i], 1);   // (counts alone: their order does not matter)
+    }
+    __syncthreads();
+    const int e = threadIdx.x;                            // (E <= 1024 threads)
+    if (e < E) {
+        int sum = 0;
+#pragma unroll 8
+        for (int w = 0; w < kPlanWarps; ++w) {
+            const int n = sh[w * E + e];
+            sh[w * E + e] = sum;
+            sum += n;
+        }
+        total[e] = sum;
+    }
+    cluster.sync();                                       // every CTA's totals are there
+    int all = 0, before = 0;                              // pairs of expert e, and those of the CTAs in front
+    if (e < E)
+        for (int r = 0; r < kPlanCtas; ++r) {
+            const int n = cluster.map_shared_rank(total, r)[e];
+            before += r < c ? n : 0;
+            all += n;
+        }
+    int upto = all;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(kFull, upto, d);
+        if (lane >= d) upto += v;
+    }
+    if (lane == 31) warp_total[warp] = upto;
+    cluster.sync();                                       // (and no CTA reads another's totals any more)
+    const int t = warp_total[lane];
+    const int first = __reduce_add_sync(kFull, lane < warp ? t : 0) + upto - all;
+    const int rows = __reduce_add_sync(kFull, t);
+    if (e < E) {
+        start[e] = first + before;
+        if (c == 0) offsets[e] = first;
+    }
+    if (c == 0 && e == 0) offsets[E] = rows;
+    for (int64_t p = (int64_t)rows + c * blockDim.x + threadIdx.x; p < P; p += kPlanCtas * blockDim.x) order[p] = -1;
+    __syncthreads();
+    const unsigned lower = (1u << lane) - 1u;
+    for (int p0 = lo; p0 < hi; p0 += 32 * kBatch) {
+        load(p0);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            unsigned same = __ballot_sync(kFull, id[i] >= 0);
+            for (int b = 0; b < id_bits; ++b) {
+                const bool bit = (id[i] >> b) & 1;
+                const unsigned with = __ballot_sync(kFull, bit);
+                same &= bit ? with : ~with;
+            }
+            if (id[i] >= 0) {
+                const int p = p0 + 32 * i + lane, row = start[id[i]] + mine[id[i]] + __popc(same & lower);
+                order[row] = p;
+                pos[p] = row;
+            }
+            __syncwarp();
+            if (id[i] >= 0 && (same & lower) == 0) mine[id[i]] += __popc(same);
+            __syncwarp();
+        }
+    }
+}
+
 // One thread sums 8 (VEC) or 1 columns of one token, the rows of up to kAhead
 // pairs in flight at once; `parts` CTAs share a token's columns.  The sum runs in
 // fp32 in the order of the pairs.  What bounds it: HBM, each row of Y read once
@@ -463,15 +613,31 @@ cudaError_t launch_route(const void *logits, int f32, const float *bias, int64_t
                          int groups, int keep, int group_top, int renorm, float scale, int *ids, float *weights,
                          int *offsets, int *order, int *pos, cudaStream_t stream)
 {
+    int lanes_log2 = 0;
+    while ((2 << lanes_log2) * groups <= 32) ++lanes_log2;
     const RouteArgs a = {logits, bias, ids, pos, offsets, order, weights, T, E, k, f32, sigmoid, groups, keep,
-                         group_top, renorm, scale};
+                         group_top, renorm, scale, E / groups, lanes_log2};
     const int64_t P = T * k;
     const bool fused = offsets && T <= kFusedWarps && P <= kFusedPairs;
     const bool simple = !bias && (groups == 1 || group_top == 1);
     const cudaError_t e = simple ? launch_experts<true>(a, fused, stream) : launch_experts<false>(a, fused, stream);
     if (e != cudaSuccess || !offsets || fused) return e;
-    const int threads = P >= 8192 ? 1024 : 256;
-    return launch_pdl(plan_kernel, dim3(E), dim3(threads), 0, stream, (const int *)ids, (int)P, E, offsets, order, pos);
+    // Both kernels for the plan after a choice, us: 4096 pairs of 128 experts 3.1 (a CTA for each expert)
+    // and 7.4 (a cluster), 65536 pairs 12 and 9.5.
+    if (P <= kPlanMany) {
+        const int threads = P >= 8192 ? 1024 : 256;
+        return launch_pdl(plan_kernel, dim3(E), dim3(threads), 0, stream, (const int *)ids, (int)P, E, offsets, order, pos);
+    }
+    const int smem = (kPlanWarps + 2) * E * (int)sizeof(int);
+    static std::atomic<bool> attr_done[kMaxDevices];
+    if (smem > 48 * 1024) {
+        const cudaError_t e2 = set_smem_attr(plan_many_kernel, (kPlanWarps + 2) * 1024 * (int)sizeof(int), attr_done);
+        if (e2 != cudaSuccess) return e2;
+    }
+    int id_bits = 0;
+    while ((1 << id_bits) < E) ++id_bits;
+    return launch_pdl(plan_many_kernel, dim3(kPlanCtas), dim3(kPlanWarps * 32), smem, stream, (const int *)ids, (int)P, E,
+                      id_bits, offsets, order, pos);
 }
 
 cudaError_t launch_combine(const void *Y, int64_t P, const int *pos, const float *weights, int64_t T, int k, int64_t N,

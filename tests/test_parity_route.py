@@ -181,12 +181,29 @@ def test_near_scores_are_told_apart(w4):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,E,k", [(5000, 24, 3), (2049, 128, 8), (8192, 256, 8), (1025, 4, 1)])
+@pytest.mark.parametrize("T,E,k", [(5000, 24, 3), (2049, 128, 8), (8192, 256, 8), (1025, 4, 1), (2731, 40, 12),
+                                   (4096, 64, 8), (4097, 64, 8), (6000, 1024, 16), (40000, 1, 1), (16500, 3, 2)])
 def test_long_plans(w4, T, E, k):
     check_ids = np.argsort(-logits(T, E, 6).astype(np.float32), axis=1, kind="stable")[:, :k].astype(np.int32)
     r = w4.route(dev_f32(logits(T, E, 6)), k)
     assert np.array_equal(r.ids.cpu().numpy(), check_ids)
     for a, b in zip((r.offsets, r.order, r.pos), plan(check_ids, E)):
+        assert np.array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k", [(300, 16, 2), (9000, 40, 4)])
+def test_long_plans_with_masked_tokens(w4, T, E, k):
+    """Pairs without an expert, in front, in the middle and at the end."""
+    x = logits(T, E, 9).astype(np.float32)
+    dead = np.random.default_rng(1).random(T) < 0.3
+    dead[:5] = dead[-7:] = True
+    x[dead] = -np.inf
+    r = w4.route(dev_f32(x), k)
+    ids = np.argsort(-x, axis=1, kind="stable")[:, :k].astype(np.int32)
+    ids[dead] = -1
+    assert np.array_equal(r.ids.cpu().numpy(), ids)
+    for a, b in zip((r.offsets, r.order, r.pos), plan(ids, E)):
         assert np.array_equal(a.cpu().numpy(), b)
 
 
