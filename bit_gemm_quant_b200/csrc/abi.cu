@@ -252,7 +252,7 @@ w4_status w4_rmsnorm(const void *X, const void *residual, const void *gamma, int
                      void *H, void *Y, uint8_t *codes, uint8_t *scales, int scale_layout, w4_stream_t stream)
 {
     if (!X || !gamma || (!Y && !codes) || (codes != nullptr) != (scales != nullptr)) return W4_ERR_INVALID_ARG;
-    if (H && !residual) return W4_ERR_INVALID_ARG;
+    if (H && (!residual || H == Y)) return W4_ERR_INVALID_ARG;
     if (scale_layout != W4_MX_SCALES_ROWS && scale_layout != W4_MX_SCALES_MMA) return W4_ERR_INVALID_ARG;
     if (M < 1 || K < 1 || !fits(w4::mx_padded_rows(M), K) || !(eps > 0.f) || isinf(eps)) return W4_ERR_INVALID_ARG;
     const size_t align = codes ? 16 : 2;

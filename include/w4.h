@@ -421,7 +421,7 @@ w4_status w4_mx_gemm(const uint8_t *x_codes, const uint8_t *x_scales, int64_t M,
  *   eps      finite, > 0.
  *   H        out, bf16 [M][K], or NULL; needs a residual.  May be the residual
  *            or X itself.
- *   Y        out, bf16 [M][K], or NULL; may be X itself.
+ *   Y        out, bf16 [M][K], or NULL; may be X itself (but not H).
  *   codes    out, uint8 [M][K] E4M3 codes, 16-byte aligned, or NULL.
  *   scales   out, E8M0 codes in `scale_layout`, as w4_mxfp8_quant writes them
  *            (W4_MX_SCALES_MMA: 16-byte aligned, padding rows 0); NULL exactly
@@ -459,8 +459,10 @@ typedef enum { W4_SOFTMAX = 0, W4_SIGMOID = 1 } w4_scoring;
  *   chosen the rest have id -1, weight 0 and position -1; a token whose logits
  *   are all -infinity (padding) gets no expert at all.  A NaN or +infinity
  *   among a token's logits gives unspecified choices and weights for that
- *   token, with ids that stay -1 or distinct and below E.  Scores that differ by less
- *   than fp64 resolves count as equal or not, whichever way they round.
+ *   token, with ids that stay -1 or distinct and below E.  With a bias, or groups
+ *   of group_top 2, scores that differ by less than fp64 resolves (and scores
+ *   below 2^-1021, which count as 0) may be equal or not, whichever way they
+ *   round; otherwise the order is that of the logits.
  *   The plan: the pairs p = t * top_k + j with an expert, sorted by expert and,
  *   for one expert, by p.
  *   logits   bf16 or fp32 [T][E], by `logits_type`; 2- or 4-byte aligned.

@@ -228,17 +228,17 @@ def test_rows_past_32_bits(w4, K):
 FAKE = 1 << 20
 
 
-def call(w4, X=FAKE, r=FAKE, gamma=FAKE, M=4, K=256, eps=1e-6, H=FAKE, Y=FAKE, codes=None, scales=None, layout=0):
+def call(w4, X=FAKE, r=FAKE, gamma=FAKE, M=4, K=256, eps=1e-6, H=FAKE + (1 << 16), Y=FAKE, codes=None, scales=None, layout=0):
     return w4.w4_rmsnorm(X, r, gamma, M, K, eps, H, Y, codes, scales, layout, None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(X=None), dict(gamma=None), dict(Y=None), dict(M=0), dict(M=-1), dict(K=0), dict(eps=0.0), dict(eps=-1.0),
-    dict(eps=float("nan")), dict(eps=float("inf")), dict(r=None), dict(X=FAKE + 1), dict(Y=FAKE + 1), dict(H=FAKE + 1),
+    dict(eps=float("nan")), dict(eps=float("inf")), dict(r=None), dict(X=FAKE + 1), dict(Y=FAKE + 1), dict(H=FAKE + (1 << 16) + 1),
     dict(codes=FAKE), dict(scales=FAKE), dict(layout=2), dict(codes=FAKE, scales=FAKE, K=40),
     dict(codes=FAKE, scales=FAKE, K=96, layout=1), dict(codes=FAKE + 8, scales=FAKE),
     dict(codes=FAKE, scales=FAKE + 8, layout=1), dict(codes=FAKE, scales=FAKE, X=FAKE + 2),
-    dict(codes=FAKE, scales=FAKE, gamma=FAKE + 8), dict(M=1 << 61, K=256)])
+    dict(codes=FAKE, scales=FAKE, gamma=FAKE + 8), dict(M=1 << 61, K=256), dict(H=FAKE + 4096, Y=FAKE + 4096)])
 def test_refusals(w4, bad):
     assert call(w4, **bad) == w4.W4_ERR_INVALID_ARG
 
