@@ -435,18 +435,21 @@ def mx_gemm(x_codes, x_scales, w_codes, w_scales, out=None, stream=None, weights
 #
 # These helpers check what the C entry points cannot see (types, shapes,
 # contiguity, one device), and run on the tensors' device, on its current
-# stream unless a ``stream=`` is given.
+# stream unless a ``stream=`` is given.  They sit in decode loops, where the
+# host's time per call counts: a call's checks are one expression (``_is``), and
+# what is wrong is only worked out (``_need``) when it is false.
 
-def _need(t, what: str, dtype, shape, like=None):
-    """ValueError unless t is a contiguous CUDA tensor of this dtype and shape, on like's device."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s: a contiguous %s tensor of shape %s is needed, got %s %s"
-                         % (what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
-    if like is None:
-        if not t.is_cuda:
-            raise ValueError("%s: a CUDA tensor is needed" % what)
-    elif t.device != like.device:
-        raise ValueError("%s is on %s, not on %s" % (what, t.device, like.device))
+def _is(t, dtype, shape, device) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()
+
+
+def _need(t, what: str, dtype, shape, device) -> None:
+    """ValueError unless t is a contiguous tensor of this dtype and shape on this CUDA device."""
+    if device.type != "cuda":
+        raise ValueError("%s: a CUDA tensor is needed" % what)
+    if not _is(t, dtype, shape, device):
+        raise ValueError("%s: a contiguous %s tensor of shape %s on %s is needed, got %s %s on %s"
+                         % (what, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
 
 
 def _placed(helper):
@@ -456,22 +459,22 @@ def _placed(helper):
     @functools.wraps(helper)
     def run(first, *args, stream=None, **kw):
         import torch
-        if stream is not None:
-            if stream.device != first.device:
-                raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, first.device))
-            with torch.cuda.stream(stream):
-                return helper(first, *args, **kw)
-        if first.is_cuda and first.device.index != torch.cuda.current_device():
+        if stream is None and (not first.is_cuda or first.get_device() == torch.cuda.current_device()):
+            return helper(first, *args, **kw)
+        if stream is None:
             with torch.cuda.device(first.device):
                 return helper(first, *args, **kw)
-        return helper(first, *args, **kw)
+        if stream.device != first.device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, first.device))
+        with torch.cuda.stream(stream):
+            return helper(first, *args, **kw)
     return run
 
 
-def _run(name: str, entry, device, *args):
-    """entry(*args, current stream); W4Error on a nonzero status."""
+def _run(name: str, index: int, *args) -> None:
+    """The entry point `name` with args and device `index`'s current stream; W4Error on a nonzero status."""
     import torch
-    st = entry(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    st = getattr(_lib or lib(), name)(*args, torch._C._cuda_getCurrentRawStream(index))
     if st != W4_OK:
         raise W4Error(st, name)
 
@@ -484,10 +487,14 @@ def _norm_checks(X, gamma, residual):
     import torch
     if X.dim() != 2:
         raise ValueError("X: a tensor of shape [M, K] is needed")
-    _need(X, "X", torch.bfloat16, X.shape)
-    _need(gamma, "gamma", torch.bfloat16, X.shape[1:], X)
-    if residual is not None:
-        _need(residual, "residual", torch.bfloat16, X.shape, X)
+    bf16, shape, dev = torch.bfloat16, X.shape, X.device
+    if not (X.is_cuda and _is(X, bf16, shape, dev) and _is(gamma, bf16, shape[1:], dev)
+            and (residual is None or _is(residual, bf16, shape, dev))):
+        _need(X, "X", bf16, shape, dev)
+        _need(gamma, "gamma", bf16, shape[1:], dev)
+        if residual is not None:
+            _need(residual, "residual", bf16, shape, dev)
+    return shape
 
 
 @_placed
@@ -497,16 +504,16 @@ def rmsnorm(X, gamma, eps: float, residual=None, out=None):
     without a residual.  ``out`` = (Y, H): Y may be X, H may be X or the
     residual."""
     import torch
-    _norm_checks(X, gamma, residual)
+    M, K = _norm_checks(X, gamma, residual)
     if out is None:
         Y, H = torch.empty_like(X), None if residual is None else torch.empty_like(X)
     else:
         Y, H = out
-        _need(Y, "out[0]", torch.bfloat16, X.shape, X)
-        if H is not None:
-            _need(H, "out[1]", torch.bfloat16, X.shape, X)
-    _run("w4_rmsnorm", lib().w4_rmsnorm, X.device, X.data_ptr(), _addr(residual), gamma.data_ptr(),
-         X.shape[0], X.shape[1], eps, _addr(H), Y.data_ptr(), None, None, MX_SCALES_ROWS)
+        for t, what in ((Y, "out[0]"), (H, "out[1]")):
+            if t is not None:
+                _need(t, what, torch.bfloat16, X.shape, X.device)
+    _run("w4_rmsnorm", X.get_device(), X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps, _addr(H), _addr(Y),
+         None, None, MX_SCALES_ROWS)
     return Y, H
 
 
@@ -516,22 +523,20 @@ def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SC
     [M, K], scales uint8 in ``scale_layout`` as ``mxfp8_quant`` gives them, H).
     ``out`` = (codes, scales, H)."""
     import torch
-    _norm_checks(X, gamma, residual)
-    M, K = X.shape
+    M, K = _norm_checks(X, gamma, residual)
     rows = scale_layout == MX_SCALES_ROWS
     if out is None:
-        codes = torch.empty((M, K), dtype=torch.uint8, device=X.device)
-        scales = torch.empty((M, max(K // 32, 1)) if rows else (max(mx_scale_bytes(M, K), 1),), dtype=torch.uint8,
-                             device=X.device)
+        codes = torch.empty_like(X, dtype=torch.uint8)
+        scales = codes.new_empty((M, max(K // 32, 1)) if rows else max(mx_scale_bytes(M, K), 1))
         H = None if residual is None else torch.empty_like(X)
     else:
         codes, scales, H = out
-        _need(codes, "out[0]", torch.uint8, X.shape, X)
-        _need(scales, "out[1]", torch.uint8, (M, K // 32) if rows else (mx_scale_bytes(M, K),), X)
+        _need(codes, "out[0]", torch.uint8, X.shape, X.device)
+        _need(scales, "out[1]", torch.uint8, (M, K // 32) if rows else (mx_scale_bytes(M, K),), X.device)
         if H is not None:
-            _need(H, "out[2]", torch.bfloat16, X.shape, X)
-    _run("w4_rmsnorm", lib().w4_rmsnorm, X.device, X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps,
-         _addr(H), None, codes.data_ptr(), scales.data_ptr(), scale_layout)
+            _need(H, "out[2]", torch.bfloat16, X.shape, X.device)
+    _run("w4_rmsnorm", X.get_device(), X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps, _addr(H), None,
+         codes.data_ptr(), scales.data_ptr(), scale_layout)
     return codes, scales, H
 
 
@@ -548,25 +553,28 @@ def route(logits, top_k: int, scoring: int = SOFTMAX, bias=None, n_groups: int =
     read).  ``bias`` (fp32 [E]) is added to the scores for the choice alone.
     Masked experts (logit -inf) are never chosen: id -1 where none is left."""
     import torch
-    if logits.dim() != 2 or logits.dtype not in (torch.float32, torch.bfloat16):
+    dtype, dev = logits.dtype, logits.device
+    f32 = dtype is torch.float32
+    if logits.dim() != 2 or not (f32 or dtype is torch.bfloat16):
         raise ValueError("logits: an fp32 or bf16 tensor of shape [T, E] is needed")
-    _need(logits, "logits", logits.dtype, logits.shape)
     T, E = logits.shape
-    if bias is not None:
-        _need(bias, "bias", torch.float32, (E,), logits)
+    if not (logits.is_cuda and logits.is_contiguous() and (bias is None or _is(bias, torch.float32, (E,), dev))):
+        _need(logits, "logits", dtype, logits.shape, dev)
+        if bias is not None:
+            _need(bias, "bias", torch.float32, (E,), dev)
     if out is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty_like(ids, dtype=torch.float32)
-        offsets, order, pos = ids.new_empty(E + 1), ids.new_empty(T * top_k), torch.empty_like(ids)
+        ids = logits.new_empty((T, top_k), dtype=torch.int32)
+        weights, pos = torch.empty_like(ids, dtype=torch.float32), torch.empty_like(ids)
+        offsets, order = ids.new_empty(E + 1), ids.new_empty(T * top_k)
     else:
         ids, weights, offsets, order, pos = out
-        for t, what, dtype, shape in ((ids, "ids", torch.int32, (T, top_k)), (weights, "weights", torch.float32, (T, top_k)),
-                                      (offsets, "offsets", torch.int32, (E + 1,)), (order, "order", torch.int32, (T * top_k,)),
-                                      (pos, "pos", torch.int32, (T, top_k))):
-            _need(t, what, dtype, shape, logits)
-    _run("w4_route", lib().w4_route, logits.device, logits.data_ptr(), 1 if logits.dtype is torch.float32 else 0,
-         _addr(bias), T, E, top_k, scoring, n_groups, topk_groups, group_top, 1 if renormalize else 0, scale,
-         ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), pos.data_ptr())
+        for t, what, dt, shape in ((ids, "ids", torch.int32, (T, top_k)), (weights, "weights", torch.float32, (T, top_k)),
+                                   (offsets, "offsets", torch.int32, (E + 1,)), (order, "order", torch.int32, (T * top_k,)),
+                                   (pos, "pos", torch.int32, (T, top_k))):
+            _need(t, what, dt, shape, dev)
+    _run("w4_route", logits.get_device(), logits.data_ptr(), 1 if f32 else 0, _addr(bias), T, E, top_k, scoring, n_groups,
+         topk_groups, group_top, 1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
+         order.data_ptr(), pos.data_ptr())
     return Routing(ids, weights, offsets, order, pos)
 
 
@@ -586,30 +594,29 @@ def experts_gemm(X, qweight, scales, qzeros, group: int, mode: int, offsets, ord
         raise ValueError("X [R, K], qweight [E, N, K/8] and a group size are needed")
     R, K = X.shape
     E, N = qweight.shape[:2]
-    _need(X, "X", torch.bfloat16, X.shape)
-    _need(qweight, "qweight", torch.int32, (E, N, K // 8), X)
-    _need(scales, "scales", torch.float16, (E, N, K // group), X)
-    if qzeros is not None:
-        _need(qzeros, "qzeros", torch.int32, (E, N, (K // group + 7) // 8), X)
-    _need(offsets, "offsets", torch.int32, (E + 1,), X)
-    P = R
-    if order is not None:
-        P = order.numel()
-        _need(order, "order", torch.int32, (P,), X)
+    dev, i32, groups = X.device, torch.int32, K // group
+    P = R if order is None else order.numel()
+    if not (X.is_cuda and _is(X, torch.bfloat16, (R, K), dev) and _is(qweight, i32, (E, N, K // 8), dev)
+            and _is(scales, torch.float16, (E, N, groups), dev) and _is(offsets, i32, (E + 1,), dev)
+            and (qzeros is None or _is(qzeros, i32, (E, N, (groups + 7) // 8), dev))
+            and (order is None or _is(order, i32, (P,), dev)) and (out is None or _is(out, torch.bfloat16, (P, N), dev))):
+        for t, what, dt, shape in ((X, "X", torch.bfloat16, (R, K)), (qweight, "qweight", i32, (E, N, K // 8)),
+                                   (scales, "scales", torch.float16, (E, N, groups)), (offsets, "offsets", i32, (E + 1,)),
+                                   (qzeros, "qzeros", i32, (E, N, (groups + 7) // 8)), (order, "order", i32, (P,)),
+                                   (out, "out", torch.bfloat16, (P, N))):
+            if t is not None:
+                _need(t, what, dt, shape, dev)
     if out is None:
-        out = torch.empty((P, N), dtype=torch.bfloat16, device=X.device)
-    else:
-        _need(out, "out", torch.bfloat16, (P, N), X)
+        out = X.new_empty((P, N))
     if workspace is None and order is not None:
-        need = lib().w4a16_experts_workspace_bytes(P, E, K, 1)
+        need = w4a16_experts_workspace_bytes(P, E, K, 1)
         if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=X.device)
-    elif workspace is not None and (workspace.device != X.device or not workspace.is_contiguous()):
-        raise ValueError("workspace: a contiguous tensor on %s is needed" % X.device)
+            workspace = X.new_empty(need, dtype=torch.uint8)
+    elif workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace: a contiguous tensor on %s is needed" % dev)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _run("w4a16_experts_gemm", lib().w4a16_experts_gemm, X.device, X.data_ptr(), R, offsets.data_ptr(),
-         _addr(order), top_k, E, P, N, K, qweight.data_ptr(), scales.data_ptr(), _addr(qzeros), group, mode,
-         out.data_ptr(), _addr(workspace), wbytes)
+    _run("w4a16_experts_gemm", X.get_device(), X.data_ptr(), R, offsets.data_ptr(), _addr(order), top_k, E, P, N, K,
+         qweight.data_ptr(), scales.data_ptr(), _addr(qzeros), group, mode, out.data_ptr(), _addr(workspace), wbytes)
     return out
 
 
@@ -621,16 +628,17 @@ def combine(Y, pos, weights, add=None, out=None):
     import torch
     if Y.dim() != 2 or pos.dim() != 2:
         raise ValueError("Y [P, N] and pos [T, top_k] are needed")
-    (P, N), (T, top_k) = Y.shape, pos.shape
-    _need(Y, "Y", torch.bfloat16, Y.shape)
-    _need(pos, "pos", torch.int32, pos.shape, Y)
-    _need(weights, "weights", torch.float32, pos.shape, Y)
-    if add is not None:
-        _need(add, "add", torch.bfloat16, (T, N), Y)
+    (P, N), (T, top_k), dev, bf16 = Y.shape, pos.shape, Y.device, torch.bfloat16
+    if not (Y.is_cuda and _is(Y, bf16, (P, N), dev) and _is(pos, torch.int32, (T, top_k), dev)
+            and _is(weights, torch.float32, (T, top_k), dev) and (add is None or _is(add, bf16, (T, N), dev))
+            and (out is None or _is(out, bf16, (T, N), dev))):
+        for t, what, dt, shape in ((Y, "Y", bf16, (P, N)), (pos, "pos", torch.int32, (T, top_k)),
+                                   (weights, "weights", torch.float32, (T, top_k)), (add, "add", bf16, (T, N)),
+                                   (out, "out", bf16, (T, N))):
+            if t is not None:
+                _need(t, what, dt, shape, dev)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.bfloat16, device=Y.device)
-    else:
-        _need(out, "out", torch.bfloat16, (T, N), Y)
-    _run("w4_combine", lib().w4_combine, Y.device, Y.data_ptr(), P, pos.data_ptr(), weights.data_ptr(), T,
-         top_k, N, _addr(add), out.data_ptr())
+        out = Y.new_empty((T, N))
+    _run("w4_combine", Y.get_device(), Y.data_ptr(), P, pos.data_ptr(), weights.data_ptr(), T, top_k, N, _addr(add),
+         out.data_ptr())
     return out
