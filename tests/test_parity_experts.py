@@ -102,7 +102,10 @@ CASES = [(1, 16, 128, 128, SYM, 1, 1), (2, 1, 32, 32, ASYM, 1, 2), (4, 40, 320, 
          (8, 300, 1408, 128, ASYM, 1, 2), (16, 64, 512, 64, SYM, 20, 4), (64, 48, 256, 32, ASYM, 16, 8),
          (5, 200, 544, 32, ASYM, 100, 2), (4, 260, 640, 128, SYM, 200, 2), (40, 130, 288, 32, ASYM, 150, 6),
          (2, 512, 1024, 128, ASYM, 700, 1), (3, 136, 2048, 64, SYM, 333, 2), (100, 32, 128, 64, ASYM, 64, 3),
-         (8, 256, 512, 128, ASYM, 1500, 2), (6, 1000, 4096, 128, ASYM, 9, 3)]
+         (8, 256, 512, 128, ASYM, 1500, 2), (6, 1000, 4096, 128, ASYM, 9, 3),
+         # the widest tiles: whole and ragged ones, stored whole or element by element
+         (2, 136, 512, 64, SYM, 1100, 1), (2, 300, 416, 32, ASYM, 1300, 1), (1, 77, 256, 128, ASYM, 600, 1),
+         (3, 128, 1088, 64, ASYM, 1000, 2), (1, 40, 32, 32, SYM, 768, 1)]
 
 
 @pytest.mark.gpu
@@ -114,7 +117,7 @@ def test_product_by_expert(w4, E, N, K, g, mode, T, k, gather):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T", [4, 90, 600])
+@pytest.mark.parametrize("T", [4, 13, 40, 90, 600, 3700])
 def test_uneven_plans(w4, T):
     """All rows at one expert; experts without rows at either end; no rows at all;
     some tokens without an expert."""
@@ -140,6 +143,41 @@ def test_same_bits_again_and_on_another_stream(w4, T):
     side.wait_stream(torch.cuda.current_stream())
     again = check(w4, layer, ids, True, stream=side)
     assert torch.equal(first[: T * 2], again[: T * 2])
+
+
+@pytest.mark.gpu
+def test_a_given_workspace(w4):
+    """A workspace of the stated size serves calls in turn; a smaller one is refused."""
+    import torch
+    layer = Layer(w4, 4, 136, 384, 64, ASYM, seed=12)
+    need = w4.w4a16_experts_workspace_bytes(400, 4, 384, 1)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")          # NaN in every place
+    for seed in (1, 2):
+        ids = random_ids(200, 4, 2, seed)
+        offsets, order = (torch.from_numpy(a).cuda() for a in plan_of(ids, 4))
+        X = dev_bf16(synth.activations(seed, 200, 384))
+        want = layer(w4, X, offsets, order=order, top_k=2)
+        assert torch.equal(layer(w4, X, offsets, order=order, top_k=2, workspace=ws), want)
+        with pytest.raises(w4.W4Error):
+            layer(w4, X, offsets, order=order, top_k=2, workspace=ws[:-256])
+
+
+@pytest.mark.gpu
+def test_tensors_on_another_device(w4):
+    """Calls on tensors of a device that is not the current one."""
+    import torch
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one GPU")
+    layer = Layer(w4, 4, 136, 384, 64, ASYM, seed=13)
+    ids = random_ids(30, 4, 2, 3)
+    offsets, order = (torch.from_numpy(a).cuda() for a in plan_of(ids, 4))
+    X = dev_bf16(synth.activations(3, 30, 384))
+    want = layer(w4, X, offsets, order=order, top_k=2)
+    to = lambda t: t.to("cuda:1")
+    got = w4.experts_gemm(to(X), to(layer.q), to(layer.s), to(layer.z), 64, ASYM, to(offsets), order=to(order), top_k=2)
+    assert got.device.index == 1 and torch.equal(got.cpu(), want.cpu())
+    with pytest.raises(ValueError):
+        w4.experts_gemm(X, to(layer.q), layer.s, layer.z, 64, ASYM, offsets, order=order, top_k=2)
 
 
 @pytest.mark.gpu
