@@ -24,9 +24,10 @@
 //     flight on an SM.  Boxes of 16 rows with 96 of them in flight on an SM fell
 //     to 2.5 TB/s (plain copies, no arithmetic; 6.3 TB/s with 48).  The ring runs
 //     on from one item to the next, so only the kernel's start waits for memory.
-//   * group constants are made once per (channel, group) and stage by one lane
-//     and shared through the warp's slot; their scales and zero-points are loaded
-//     a stage ahead, and asked into L2 when the ring reaches their item.
+//   * group constants are made once per (channel, group) and stage, lane l making
+//     those of channel l, and shared through the warp's slot; their scales (one
+//     load) and zero-points are loaded a stage ahead, and asked into L2 when the
+//     ring reaches their item.
 //   * activations come through L1 (the warps of an SM mostly read the same rows),
 //     a stage's 64 bytes of each half in flight before the stage waits for its
 //     codes; all CTAs together ask X into L2 at the start.
@@ -58,13 +59,13 @@ constexpr int kRedBytes = kC * 32 * 16;              // one warp's partial tile
 template <int G>
 struct ExpCfg {
     static constexpr int kGroups = kSK / G;
-    static constexpr int kCpl = kRows * kGroups / 32;                  // constants per lane and stage
     static constexpr int kConstOff = kNW * kR * kStageBytes;
-    static constexpr int kRedOff = kConstOff + kNW * 32 * kCpl * 8;
+    static constexpr int kRedOff = kConstOff + kNW * kRows * kGroups * 8;
     static constexpr int kBarOff = kRedOff + 2 * kNW * kRedBytes;
     static constexpr int kPlanOff = kBarOff + (kNW * kR + 1) * 8 + 8;  // + the stall barrier, the failure flag
     static int bytes(int E) { return kPlanOff + (2 * E + 1) * 4 + 1024; }
 };
+static_assert(kRows == 32, "a lane for each channel of an item");
 static_assert(kCtas * (ExpCfg<32>::kPlanOff + 2049 * 4 + 2048) <= 228 * 1024, "shared memory of the resident CTAs");
 
 __device__ __noinline__ bool wait_copy(uint32_t bar, uint32_t parity, uint64_t limit)
@@ -150,7 +151,7 @@ experts_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *
     const uint64_t limit = wait_limit_of(wait_ns);
 
     uint8_t *ring = smem + warp * kR * kStageBytes;
-    uint2 *cslot = (uint2 *)(smem + Cfg::kConstOff) + warp * 32 * Cfg::kCpl;
+    uint2 *cslot = (uint2 *)(smem + Cfg::kConstOff) + warp * kRows * Cfg::kGroups;
     const uint32_t ring_s = smem_u32(ring);
     const uint32_t bar0 = smem_u32(smem + Cfg::kBarOff) + warp * kR * 8;
     const uint32_t stall_bar = smem_u32(smem + Cfg::kBarOff) + kNW * kR * 8;
@@ -249,17 +250,38 @@ experts_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *
         }
     };
 
-    // ---- scales and zero-points of one stage, held by the lanes that make its constants ----
-    unsigned short sv[Cfg::kCpl];
-    uint32_t zv[Cfg::kCpl];
+    // ---- scales and zero-points of one stage: lane l holds those of the item's channel l ----
+    // (the kGroups scales of a stage are one load where rows of scales are whole stages, and their
+    // zero-points lie in one word)
+    constexpr int kGroups = Cfg::kGroups;
+    const bool whole = NG % kGroups == 0 && (uintptr_t)scales % (2 * kGroups) == 0;
+    uint32_t sv[kGroups / 2], zv = 0;
     auto load_consts = [&](int row0, int rows, int stage) {   // row0: in the arrays; rows: valid ones
 #pragma unroll
-        for (int u = 0; u < Cfg::kCpl; ++u) {
-            const int idx = lane + 32 * u, r = idx % kRows, jg = stage * Cfg::kGroups + idx / kRows;
-            const bool ok = r < rows && jg < NG;
-            sv[u] = ok ? __ldg(scales + (size_t)(row0 + r) * NG + jg) : (unsigned short)0;
-            if (MODE == W4_ASYM) zv[u] = ok ? __ldg(qzeros + (size_t)(row0 + r) * ZW + (jg >> 3)) : 0u;
+        for (int u = 0; u < kGroups / 2; ++u) sv[u] = 0;
+        if (lane >= rows) return;
+        const int j0 = stage * kGroups;
+        const unsigned short *p = scales + (size_t)(row0 + lane) * NG + j0;
+        if (whole) {
+            if constexpr (kGroups == 2) sv[0] = __ldg((const uint32_t *)p);
+            if constexpr (kGroups == 4) {
+                const uint2 v = __ldg((const uint2 *)p);
+                sv[0] = v.x;
+                sv[1] = v.y;
+            }
+            if constexpr (kGroups == 8) {
+                const uint4 v = __ldg((const uint4 *)p);
+                sv[0] = v.x;
+                sv[1] = v.y;
+                sv[2] = v.z;
+                sv[3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int u = 0; u < kGroups; ++u)
+                if (j0 + u < NG) sv[u / 2] |= (uint32_t)__ldg(p + u) << (16 * (u & 1));
         }
+        if (MODE == W4_ASYM) zv = __ldg(qzeros + (size_t)(row0 + lane) * ZW + (j0 >> 3));
     };
 
     const uint32_t magic = 0x43004300u;               // bf16x2 of (128, 128)
@@ -315,11 +337,11 @@ experts_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *
                 for (int w = 0; w < 4; ++w) x[4 * odd + w] = __ldg(p + w);
             }
             __syncwarp();                              // every lane is done with the previous stage's constants
+            // (nothing has looked at the loaded words before: the loads had a stage's time)
 #pragma unroll
-            for (int q = 0; q < Cfg::kCpl; ++q) {
-                // (nothing has looked at the loaded words before: the loads had a stage's time)
-                const int jg = st * Cfg::kGroups + (lane + 32 * q) / kRows;
-                const GroupConst gc = group_const(sv[q], MODE == W4_ASYM ? (zv[q] >> (4 * (jg & 7))) & 15u : 8u);
+            for (int q = 0; q < kGroups; ++q) {
+                const uint32_t zp = MODE == W4_ASYM ? (zv >> (4 * ((st * kGroups + q) & 7))) & 15u : 8u;
+                const GroupConst gc = group_const((unsigned short)(sv[q / 2] >> (16 * (q & 1))), zp);
                 cslot[lane + 32 * q] = make_uint2(__byte_perm(gc.shi, gc.slo, 0x5410), gc.z);
             }
             if (st + KS < NS) load_consts(row0, N - r0, st + KS);
