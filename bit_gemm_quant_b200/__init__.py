@@ -11,7 +11,6 @@ missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from collections import namedtuple
 
@@ -452,23 +451,20 @@ def _need(t, what: str, dtype, shape, device) -> None:
                          % (what, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device))
 
 
-def _placed(helper):
-    """Runs a helper with its first tensor's device current and, where ``stream``
-    is given, that stream: outputs and scratch are allocated on the stream that
+def _elsewhere(helper, stream, first, *args):
+    """helper(first, *args) with `first`'s device current and, where a stream is
+    given, that stream: outputs and scratch are allocated on the stream that
     writes them."""
-    @functools.wraps(helper)
-    def run(first, *args, stream=None, **kw):
-        import torch
-        if stream is None and (not first.is_cuda or first.get_device() == torch.cuda.current_device()):
-            return helper(first, *args, **kw)
-        if stream is None:
-            with torch.cuda.device(first.device):
-                return helper(first, *args, **kw)
-        if stream.device != first.device:
-            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, first.device))
-        with torch.cuda.stream(stream):
-            return helper(first, *args, **kw)
-    return run
+    import torch
+    if not first.is_cuda:
+        raise ValueError("%s: CUDA tensors are needed" % helper.__name__)
+    if stream is None:
+        with torch.cuda.device(first.device):
+            return helper(first, *args)
+    if stream.device != first.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, first.device))
+    with torch.cuda.stream(stream):
+        return helper(first, *args)
 
 
 def _run(name: str, index: int, *args) -> None:
@@ -488,7 +484,7 @@ def _norm_checks(X, gamma, residual):
     if X.dim() != 2:
         raise ValueError("X: a tensor of shape [M, K] is needed")
     bf16, shape, dev = torch.bfloat16, X.shape, X.device
-    if not (X.is_cuda and _is(X, bf16, shape, dev) and _is(gamma, bf16, shape[1:], dev)
+    if not (X.dtype is bf16 and X.is_contiguous() and _is(gamma, bf16, shape[1:], dev)
             and (residual is None or _is(residual, bf16, shape, dev))):
         _need(X, "X", bf16, shape, dev)
         _need(gamma, "gamma", bf16, shape[1:], dev)
@@ -497,13 +493,15 @@ def _norm_checks(X, gamma, residual):
     return shape
 
 
-@_placed
-def rmsnorm(X, gamma, eps: float, residual=None, out=None):
+def rmsnorm(X, gamma, eps: float, residual=None, out=None, stream=None):
     """RMS norm of the rows of X[M,K] (bf16 CUDA): returns (Y, H) in bf16 with
     h = X + residual, Y = h / sqrt(mean h^2 + eps) * gamma and H = h; H is None
     without a residual.  ``out`` = (Y, H): Y may be X, H may be X or the
     residual."""
     import torch
+    index = X.get_device()
+    if stream is not None or index < 0 or index != torch._C._cuda_getDevice():
+        return _elsewhere(rmsnorm, stream, X, gamma, eps, residual, out)
     M, K = _norm_checks(X, gamma, residual)
     if out is None:
         Y, H = torch.empty_like(X), None if residual is None else torch.empty_like(X)
@@ -512,17 +510,19 @@ def rmsnorm(X, gamma, eps: float, residual=None, out=None):
         for t, what in ((Y, "out[0]"), (H, "out[1]")):
             if t is not None:
                 _need(t, what, torch.bfloat16, X.shape, X.device)
-    _run("w4_rmsnorm", X.get_device(), X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps, _addr(H), _addr(Y),
+    _run("w4_rmsnorm", index, X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps, _addr(H), _addr(Y),
          None, None, MX_SCALES_ROWS)
     return Y, H
 
 
-@_placed
-def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SCALES_MMA, out=None):
+def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SCALES_MMA, out=None, stream=None):
     """``rmsnorm`` quantized to MXFP8 in the same pass: returns (codes uint8
     [M, K], scales uint8 in ``scale_layout`` as ``mxfp8_quant`` gives them, H).
     ``out`` = (codes, scales, H)."""
     import torch
+    index = X.get_device()
+    if stream is not None or index < 0 or index != torch._C._cuda_getDevice():
+        return _elsewhere(rmsnorm_mxfp8, stream, X, gamma, eps, residual, scale_layout, out)
     M, K = _norm_checks(X, gamma, residual)
     rows = scale_layout == MX_SCALES_ROWS
     if out is None:
@@ -535,7 +535,7 @@ def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SC
         _need(scales, "out[1]", torch.uint8, (M, K // 32) if rows else (mx_scale_bytes(M, K),), X.device)
         if H is not None:
             _need(H, "out[2]", torch.bfloat16, X.shape, X.device)
-    _run("w4_rmsnorm", X.get_device(), X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps, _addr(H), None,
+    _run("w4_rmsnorm", index, X.data_ptr(), _addr(residual), gamma.data_ptr(), M, K, eps, _addr(H), None,
          codes.data_ptr(), scales.data_ptr(), scale_layout)
     return codes, scales, H
 
@@ -543,9 +543,8 @@ def rmsnorm_mxfp8(X, gamma, eps: float, residual=None, scale_layout: int = MX_SC
 Routing = namedtuple("Routing", "ids weights offsets order pos")
 
 
-@_placed
 def route(logits, top_k: int, scoring: int = SOFTMAX, bias=None, n_groups: int = 1, topk_groups: int = 1,
-          group_top: int = 1, renormalize: bool = True, scale: float = 1.0, out=None):
+          group_top: int = 1, renormalize: bool = True, scale: float = 1.0, out=None, stream=None):
     """Routing of the tokens behind logits[T,E] (fp32 or bf16 CUDA) to top_k of
     E experts: a ``Routing`` of ids int32 [T, top_k], weights fp32 [T, top_k] and
     the plan of the experts' rows: offsets int32 [E + 1], order int32
@@ -553,34 +552,38 @@ def route(logits, top_k: int, scoring: int = SOFTMAX, bias=None, n_groups: int =
     read).  ``bias`` (fp32 [E]) is added to the scores for the choice alone.
     Masked experts (logit -inf) are never chosen: id -1 where none is left."""
     import torch
+    index = logits.get_device()
+    if stream is not None or index < 0 or index != torch._C._cuda_getDevice():
+        return _elsewhere(route, stream, logits, top_k, scoring, bias, n_groups, topk_groups, group_top, renormalize, scale,
+                          out)
     dtype, dev = logits.dtype, logits.device
     f32 = dtype is torch.float32
     if logits.dim() != 2 or not (f32 or dtype is torch.bfloat16):
         raise ValueError("logits: an fp32 or bf16 tensor of shape [T, E] is needed")
     T, E = logits.shape
-    if not (logits.is_cuda and logits.is_contiguous() and (bias is None or _is(bias, torch.float32, (E,), dev))):
+    if not (logits.is_contiguous() and (bias is None or _is(bias, torch.float32, (E,), dev))):
         _need(logits, "logits", dtype, logits.shape, dev)
         if bias is not None:
             _need(bias, "bias", torch.float32, (E,), dev)
     if out is None:
-        ids = logits.new_empty((T, top_k), dtype=torch.int32)
-        weights, pos = torch.empty_like(ids, dtype=torch.float32), torch.empty_like(ids)
-        offsets, order = ids.new_empty(E + 1), ids.new_empty(T * top_k)
+        new, i32, shape, strides = torch.empty_strided, torch.int32, (T, top_k), (top_k, 1)
+        ids = new(shape, strides, dtype=i32, device=dev)
+        weights, pos = new(shape, strides, dtype=torch.float32, device=dev), torch.empty_like(ids)
+        offsets, order = new((E + 1,), (1,), dtype=i32, device=dev), new((T * top_k,), (1,), dtype=i32, device=dev)
     else:
         ids, weights, offsets, order, pos = out
         for t, what, dt, shape in ((ids, "ids", torch.int32, (T, top_k)), (weights, "weights", torch.float32, (T, top_k)),
                                    (offsets, "offsets", torch.int32, (E + 1,)), (order, "order", torch.int32, (T * top_k,)),
                                    (pos, "pos", torch.int32, (T, top_k))):
             _need(t, what, dt, shape, dev)
-    _run("w4_route", logits.get_device(), logits.data_ptr(), 1 if f32 else 0, _addr(bias), T, E, top_k, scoring, n_groups,
+    _run("w4_route", index, logits.data_ptr(), 1 if f32 else 0, _addr(bias), T, E, top_k, scoring, n_groups,
          topk_groups, group_top, 1 if renormalize else 0, scale, ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(),
          order.data_ptr(), pos.data_ptr())
     return Routing(ids, weights, offsets, order, pos)
 
 
-@_placed
 def experts_gemm(X, qweight, scales, qzeros, group: int, mode: int, offsets, order=None, top_k: int = 1,
-                 workspace=None, out=None):
+                 workspace=None, out=None, stream=None):
     """The W4A16 product by expert: Y[i] = X[row] . W[e]^T for the sorted rows
     offsets[e] <= i < offsets[e + 1] of a ``route`` plan, row = order[i] // top_k
     (i itself without ``order``: X holds the sorted rows already).  qweight int32
@@ -590,13 +593,17 @@ def experts_gemm(X, qweight, scales, qzeros, group: int, mode: int, offsets, ord
     written.  ``workspace``: w4a16_experts_workspace_bytes(...) bytes of CUDA
     memory (allocated per call where it is needed and not given)."""
     import torch
+    index = X.get_device()
+    if stream is not None or index < 0 or index != torch._C._cuda_getDevice():
+        return _elsewhere(experts_gemm, stream, X, qweight, scales, qzeros, group, mode, offsets, order, top_k, workspace,
+                          out)
     if X.dim() != 2 or qweight.dim() != 3 or group < 1:
         raise ValueError("X [R, K], qweight [E, N, K/8] and a group size are needed")
     R, K = X.shape
     E, N = qweight.shape[:2]
     dev, i32, groups = X.device, torch.int32, K // group
     P = R if order is None else order.numel()
-    if not (X.is_cuda and _is(X, torch.bfloat16, (R, K), dev) and _is(qweight, i32, (E, N, K // 8), dev)
+    if not (_is(X, torch.bfloat16, (R, K), dev) and _is(qweight, i32, (E, N, K // 8), dev)
             and _is(scales, torch.float16, (E, N, groups), dev) and _is(offsets, i32, (E + 1,), dev)
             and (qzeros is None or _is(qzeros, i32, (E, N, (groups + 7) // 8), dev))
             and (order is None or _is(order, i32, (P,), dev)) and (out is None or _is(out, torch.bfloat16, (P, N), dev))):
@@ -607,7 +614,7 @@ def experts_gemm(X, qweight, scales, qzeros, group: int, mode: int, offsets, ord
             if t is not None:
                 _need(t, what, dt, shape, dev)
     if out is None:
-        out = X.new_empty((P, N))
+        out = torch.empty_strided((P, N), (N, 1), dtype=torch.bfloat16, device=dev)
     if workspace is None and order is not None:
         need = w4a16_experts_workspace_bytes(P, E, K, 1)
         if need:
@@ -615,21 +622,23 @@ def experts_gemm(X, qweight, scales, qzeros, group: int, mode: int, offsets, ord
     elif workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
         raise ValueError("workspace: a contiguous tensor on %s is needed" % dev)
     wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _run("w4a16_experts_gemm", X.get_device(), X.data_ptr(), R, offsets.data_ptr(), _addr(order), top_k, E, P, N, K,
+    _run("w4a16_experts_gemm", index, X.data_ptr(), R, offsets.data_ptr(), _addr(order), top_k, E, P, N, K,
          qweight.data_ptr(), scales.data_ptr(), _addr(qzeros), group, mode, out.data_ptr(), _addr(workspace), wbytes)
     return out
 
 
-@_placed
-def combine(Y, pos, weights, add=None, out=None):
+def combine(Y, pos, weights, add=None, out=None, stream=None):
     """out[t] = add[t] + sum_j weights[t, j] * Y[pos[t, j]] (bf16 [T, N]) from an
     ``experts_gemm`` result Y[P, N] and a ``route`` plan's pos and weights
     [T, top_k]; positions of -1 add nothing.  ``out`` may be ``add``."""
     import torch
+    index = Y.get_device()
+    if stream is not None or index < 0 or index != torch._C._cuda_getDevice():
+        return _elsewhere(combine, stream, Y, pos, weights, add, out)
     if Y.dim() != 2 or pos.dim() != 2:
         raise ValueError("Y [P, N] and pos [T, top_k] are needed")
     (P, N), (T, top_k), dev, bf16 = Y.shape, pos.shape, Y.device, torch.bfloat16
-    if not (Y.is_cuda and _is(Y, bf16, (P, N), dev) and _is(pos, torch.int32, (T, top_k), dev)
+    if not (Y.dtype is bf16 and Y.is_contiguous() and _is(pos, torch.int32, (T, top_k), dev)
             and _is(weights, torch.float32, (T, top_k), dev) and (add is None or _is(add, bf16, (T, N), dev))
             and (out is None or _is(out, bf16, (T, N), dev))):
         for t, what, dt, shape in ((Y, "Y", bf16, (P, N)), (pos, "pos", torch.int32, (T, top_k)),
@@ -638,7 +647,7 @@ def combine(Y, pos, weights, add=None, out=None):
             if t is not None:
                 _need(t, what, dt, shape, dev)
     if out is None:
-        out = Y.new_empty((T, N))
-    _run("w4_combine", Y.get_device(), Y.data_ptr(), P, pos.data_ptr(), weights.data_ptr(), T, top_k, N, _addr(add),
+        out = torch.empty_strided((T, N), (N, 1), dtype=bf16, device=dev)
+    _run("w4_combine", index, Y.data_ptr(), P, pos.data_ptr(), weights.data_ptr(), T, top_k, N, _addr(add),
          out.data_ptr())
     return out
