@@ -121,13 +121,6 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int n0 = blockIdx.x * 128, nkb = (K + kKB - 1) / kKB;
 
-    pdl_wait();                                                        // the plan is there
-    pdl_launch_dependents();
-    const ExpertUnit unit = find_unit(plan, blockIdx.y, BN);
-    if (unit.rows == 0) return;                                        // (every warp finds the same)
-    const int m0 = unit.row0, q0 = unit.expert * N + n0;
-    const bool tile_store = y_tma && unit.rows == BN;                  // no other expert's rows in the tile
-
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full_b[s], 1);
@@ -144,10 +137,20 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) tmem_alloc(tmem_slot, C::kCols);
+    pdl_wait();                                                        // the plan is there
+    pdl_launch_dependents();
+    const ExpertUnit unit = find_unit(plan, blockIdx.y, BN);           // (every warp finds the same)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (unit.rows == 0) {                                              // fewer units than the grid has room for
+        __syncthreads();
+        if (warp == 1) tmem_dealloc(tmem, C::kCols);
+        return;
+    }
+    const int m0 = unit.row0, q0 = unit.expert * N + n0;
+    const bool tile_store = y_tma && unit.rows == BN;                  // no other expert's rows in the tile
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer --
