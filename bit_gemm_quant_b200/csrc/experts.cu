@@ -9,15 +9,15 @@
 // dequantization 19/8 instructions, 12/8 of them bf16x2 operations, of which an
 // SM starts two per clock (measured; fp32 FMAs start four): 256 weights take 6
 // clocks at least, 12.0e12 weights/s on 148 SMs, the same as the 12.6e12 that
-// HBM delivers.  The kernel runs 3.55 instructions a weight.  Measured for one
+// HBM delivers.  The kernel runs about 3.5 instructions a weight.  Measured for one
 // token and 2 of 8 experts [14336, 4096], asymmetric, g = 128 (61 MB, 9.3 us of
-// HBM): 26.8 us, of which the copies alone are 13.1 us (kernel start and plan
+// HBM): 26.2 us, of which the copies alone are 13.1 us (kernel start and plan
 // 1.3, first copies 2.5) and the dequantization's instructions 9.6 us; 16 tokens
-// and 8 of 64 experts [2048, 2048], symmetric, g = 64: 39.7 us (19.3 of HBM).
+// and 8 of 64 experts [2048, 2048], symmetric, g = 64: 38.1 us (19.3 of HBM).
 //   * warps are persistent.  A work item is (unit, tile): up to 8 rows of one
 //     expert (the columns of an MMA) and 32 of its channels, two MMA tiles that
-//     share the activations (one tile an item: 16 tokens above take 50 us; four:
-//     61).  A team of KS warps shares an item, warp j taking the 256-k stages j,
+//     share the activations (with one tile an item the 16 tokens above took 50 us,
+//     with four 61, with two 41 at that stage).  A team of KS warps shares an item, warp j taking the 256-k stages j,
 //     j + KS, ...; teams take items in turn.
 //   * the codes come by TMA, one box of 32 rows x 256 k (128-byte swizzle) a
 //     stage, two stages ahead on the warp's own ring of mbarriers, 128 KB in

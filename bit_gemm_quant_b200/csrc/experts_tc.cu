@@ -23,7 +23,7 @@
 // looked at only where they are used.  8 of 8 experts [14336, 4096] with 8 rows
 // each: 106 us (37.6 of HBM).  With many rows, copies (576 clocks a k-block of 256
 // rows at 64 bytes a clock) and MMAs (512) alike: 8192 tokens, 2 of 8 experts:
-// 1694 us, 1136 TFLOP/s, 82% of the sustained cuBLAS rate (1828 with w4a16_gemm's
+// 1672 us, 1151 TFLOP/s, 83% of the sustained cuBLAS rate (1828 with w4a16_gemm's
 // loop by expert).
 #include "experts.cuh"
 #include "tc_pipe.cuh"
