@@ -18,8 +18,9 @@
 // One warp chooses for one token: lane l holds the experts l, l + 32, ..., so
 // logits are read in whole lines and equal choices can be told apart by index.
 // A choice is compared as an integer in the order of the floating values (masked
-// experts 0, below every number); its maximum over the warp takes two 32-bit
-// reductions (three for fp64): the key, then the lowest index that has it.
+// experts 0, below every number); its maximum over the warp takes one 32-bit
+// reduction, a ballot and a shuffle, and two reductions more only where several
+// lanes share the largest (high) word.
 //
 // The plan of up to kPlanMany pairs needs no scan across CTAs: the CTA of expert e
 // reads all ids, counts those below e (where its rows begin) and lists its own
