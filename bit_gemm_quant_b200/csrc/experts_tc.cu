@@ -12,18 +12,18 @@
 // B = the rows by TMA, one warp for the copies, one thread for the MMAs.  CTA
 // (x, y) owns the channels 128 x .. of one expert and up to BN of that expert's
 // rows (unit y of the plan); N and the channels are per expert.  A box's rows
-// past the unit's are other rows of X, whose accumulator columns are never
-// stored; a whole tile of rows leaves by TMA, a ragged one by plain stores.
+// past the unit's are other rows of X: the MMAs leave them out from the next
+// multiple of 16 on, and their accumulator columns are never stored; a whole tile of rows leaves by TMA, a ragged one by plain stores.
 //
 // What bounds it.  With few rows an expert, the dequantization: 157 instructions
 // per warp and k-block (2.4 a weight), whatever BN is, in whose way the MMA
-// issuer has to find its slots (about 125 clocks an MMA at 64 rows, 45 alone).  So
+// issuer has to find its slots (about 125 clocks an MMA of 64 rows, 45 alone).  So
 // group size and mode are template parameters here, the loop is unrolled over the
 // ring, and a group's scale and zero-point word are loaded a round ahead and
 // looked at only where they are used.  8 of 8 experts [14336, 4096] with 8 rows
-// each: 106 us (37.6 of HBM).  With many rows, copies (576 clocks a k-block of 256
+// each: 105 us (37.6 of HBM).  With many rows, copies (576 clocks a k-block of 256
 // rows at 64 bytes a clock) and MMAs (512) alike: 8192 tokens, 2 of 8 experts:
-// 1672 us, 1151 TFLOP/s, 83% of the sustained cuBLAS rate (1828 with w4a16_gemm's
+// 1647 us, 1168 TFLOP/s, 84% of the sustained cuBLAS rate (1828 with w4a16_gemm's
 // loop by expert).
 #include "experts.cuh"
 #include "tc_pipe.cuh"
@@ -86,7 +86,7 @@ __device__ __forceinline__ bool mma_kblock_warp(uint32_t leader, uint32_t d_tmem
 template <int BN>
 struct ExpTcCfg {
     using C = TcCfg<BN>;
-    static constexpr int kCodes = BN <= 64 ? 3 : 2;
+    static constexpr int kCodes = 2;
     static constexpr int kCodeBytes = 128 * 128;
     static constexpr int kCodeOff = C::kStages * C::kBBytes;
     static constexpr int kBarOff = kCodeOff + kCodes * kCodeBytes;
@@ -198,6 +198,11 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         // ------------------------------------------------- MMA issuer ---
         const uint32_t leader = elect_one();
         const uint32_t tmem_u = __shfl_sync(0xffffffffu, tmem, 0);
+        // an MMA as wide as the unit's rows, in steps of 16 (N / 8 stands in the descriptor from bit 17 on):
+        // 8 experts [14336, 4096], 64 rows each: 129 -> 113 us, 1024: 785 -> 760.  (X by boxes of the rows
+        // that are there, 16 to 64 at a time, was slower: 3 to 40 %.)
+        const uint32_t idesc = __shfl_sync(
+            0xffffffffu, (C::kIdesc & ~(0x3Fu << 17)) | ((uint32_t)((unit.rows + 15) / 16 * 2) << 17), 0);
         const uint64_t bdesc0 = desc_k_sw128(smem_u32(sB));
         const uint32_t fa0 = smem_u32(full_a), fb0 = smem_u32(full_b), em0 = smem_u32(empty);
         bool ready = false, stop = false;
@@ -220,7 +225,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
                 const uint32_t ph1 = (st + 1 == kStages) ? (ph ^ 1u) : ph;
                 const bool last = i + 1 == nkb;
                 ready = mma_kblock_warp(leader, tmem_u, tmem_u + C::kACol0 + st * 32,
-                                        bdesc0 + (uint64_t)((st * C::kBBytes) >> 4), C::kIdesc, i > 0 ? 1u : 0u,
+                                        bdesc0 + (uint64_t)((st * C::kBBytes) >> 4), idesc, i > 0 ? 1u : 0u,
                                         em0 + 8 * st, fa0 + 8 * (last ? st : s1), fb0 + 8 * (last ? st : s1),
                                         last ? ph : ph1);
             }
@@ -325,7 +330,7 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         const bool have = __all_sync(0xffffffffu, ok && wait_bounded(done, 0, abort_flag, err, kErrWaitDone, limit));
         tc_fence_after();
         constexpr int HALF = BN / 2;                  // columns per warp of a lane quarter
-        constexpr int CH = HALF < 64 ? HALF : 64;     // and per round of loads
+        constexpr int CH = 64;                        // and per round of loads
         const int cbeg = h * HALF;
         if (have) {
             // a whole tile goes through the (now idle) stage buffers, stored below by one TMA; every warp
@@ -333,13 +338,8 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
             __nv_bfloat16 *ysm = (__nv_bfloat16 *)smem;
             for (int c = cbeg; c < cbeg + HALF && c < unit.rows; c += CH) {
                 float acc[CH];
-                if (CH >= 32) {
 #pragma unroll
-                    for (int u = 0; u < CH / 32; ++u) tmem_ld32(lane_addr + c + 32 * u, acc + 32 * u);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < CH / 8; ++u) tmem_ld8(lane_addr + c + 8 * u, acc + 8 * u);
-                }
+                for (int u = 0; u < CH / 32; ++u) tmem_ld32(lane_addr + c + 32 * u, acc + 32 * u);
                 tmem_wait_ld();
                 if (tile_store) {
 #pragma unroll
@@ -396,8 +396,8 @@ template <int BN, int G, int MODE>
 cudaError_t launch_tc(const TcMaps &m, const ExpertPlan &plan, int N, int K, const void *scales, const uint32_t *qzeros,
                       void *Y, int *err, cudaStream_t stream)
 {
-    int smem = ExpTcCfg<BN>::kBytes;
-    if (TcCfg<BN>::kMinBlocks == 2 && smem < 80 * 1024) smem = 80 * 1024;   // at most 2 CTAs share an SM's tensor memory
+    constexpr int smem = ExpTcCfg<BN>::kBytes;
+    static_assert(smem * 3 > 227 * 1024, "an SM's tensor memory holds two CTAs at most");
     static std::atomic<bool> attr_done[kMaxDevices];
     auto kern = experts_tc_kernel<BN, G, MODE>;
     const cudaError_t e = set_smem_attr(kern, smem, attr_done);
@@ -412,7 +412,6 @@ cudaError_t launch_tc_bn(int BN, const TcMaps &m, const ExpertPlan &plan, int N,
                          const uint32_t *qzeros, void *Y, int *err, cudaStream_t stream)
 {
     switch (BN) {
-    case 64: return launch_tc<64, G, MODE>(m, plan, N, K, scales, qzeros, Y, err, stream);
     case 128: return launch_tc<128, G, MODE>(m, plan, N, K, scales, qzeros, Y, err, stream);
     default: return launch_tc<256, G, MODE>(m, plan, N, K, scales, qzeros, Y, err, stream);
     }
@@ -439,12 +438,14 @@ cudaError_t launch_experts_tc(const void *X, ExpertPlan plan, int64_t N, int64_t
         plan.order = nullptr;
     }
     // Rows of a tile by the rows an expert has on average: a larger tile shares a dequantized weight
-    // among more rows, a smaller one computes less past an expert's last.  Measured, us with 64 / 128 /
-    // 256: 8 experts [14336, 4096] at 32 rows each 110 / 119 / 170, 64: 155 / 128 / 181, 256: 408 / 275 /
-    // 291, 1024: 1390 / 895 / 807; 64 of [2048, 2048] at 32: 78 / 80 / 118, 256: 280 / 193 / 200.  (32
-    // rows were never faster than 64.)
+    // among more rows, a smaller one has two CTAs on an SM.  (What an MMA computes past an expert's
+    // last row is the same with both: at most 15 rows.)  Measured, us with 128 / 256: 8 experts
+    // [14336, 4096] at 32 rows each 108 / 148, 64: 113 / 152, 200: 220 / 213, 256: 265 / 257,
+    // 1024: 884 / 760; 64 of [2048, 2048] at 32: 71 / 97, 200: 151 / 158, 256: 186 / 181, 1024:
+    // 619 / 569; 128 of [768, 2048] at 200: 136 / 143, 300: 186 / 184.  (Tiles of 64 rows are within
+    // 2 % of 128's up to 12 rows an expert, on either side, and slower beyond.)
     const int64_t rows = plan.P / plan.E;
-    const int BN = rows <= 40 ? 64 : rows <= 512 ? 128 : 256;
+    const int BN = rows <= 224 ? 128 : 256;
     TcMaps m;
     const cuuint32_t estride[2] = {1, 1};
     const cuuint64_t gdim[2] = {(cuuint64_t)K, (cuuint64_t)plan.P};
