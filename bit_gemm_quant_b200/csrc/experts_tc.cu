@@ -122,6 +122,8 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     const int n0 = blockIdx.x * 128, nkb = (K + kKB - 1) / kKB;
 
     if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmap_x) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&tmap_q) : "memory");
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full_b[s], 1);
             mbar_init(&full_a[s], 4);
@@ -274,13 +276,22 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
                 const int v = v0 + u;
                 if (h + 2 * v >= nkb || !ok) break;
                 const int s = h + 2 * u;
+                const int j = j0 + v * kStep;
+                if (MODE == W4_ASYM && v > 0 && (v & (8 / kStep - 1)) == 0) {
+                    zcur = znext;
+                    znext = zword((j >> 3) + 1);
+                }
+                const GroupConst c0 = group_const(s0[u], MODE == W4_ASYM ? (zcur >> (4 * (j & 7))) & 15u : 8u);
+                const GroupConst c1 =
+                    G == 32 ? group_const(s1[u], MODE == W4_ASYM ? (zcur >> (4 * ((j + 1) & 7))) & 15u : 8u) : c0;
                 // the codes (a box holds two k-blocks of each warp), and the stage's tensor-memory columns:
                 // the MMAs of its previous round are done
                 // (the first wait targets a barrier that nothing completes in the failure-path tests)
                 uint64_t *fc = (v == 0 && stalls_first_wait(wait_ns)) ? stall : &full_c[cs];
                 const uint32_t fph = fc == stall ? 0u : cph;
                 if (!__all_sync(0xffffffffu,
-                                (mbar_try_wait(fc, fph) || wait_bounded(fc, fph, abort_flag, err, kErrWaitTma, limit)) &&
+                                ((v & 1) || mbar_try_wait(fc, fph) ||
+                                 wait_bounded(fc, fph, abort_flag, err, kErrWaitTma, limit)) &&
                                     (mbar_try_wait(&empty[s], ph ^ 1) ||
                                      wait_bounded(&empty[s], ph ^ 1, abort_flag, err, kErrWaitEmptyDeq, limit)))) {
                     ok = false;
@@ -291,14 +302,6 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
                 const int chunk = 2 * h + 4 * (v & 1);
                 const uint4 w0 = *(const uint4 *)(row + ((chunk ^ (r & 7)) << 4));
                 const uint4 w1 = *(const uint4 *)(row + (((chunk + 1) ^ (r & 7)) << 4));
-                const int j = j0 + v * kStep;
-                if (MODE == W4_ASYM && v > 0 && (v & (8 / kStep - 1)) == 0) {
-                    zcur = znext;
-                    znext = zword((j >> 3) + 1);
-                }
-                const GroupConst c0 = group_const(s0[u], MODE == W4_ASYM ? (zcur >> (4 * (j & 7))) & 15u : 8u);
-                const GroupConst c1 =
-                    G == 32 ? group_const(s1[u], MODE == W4_ASYM ? (zcur >> (4 * ((j + 1) & 7))) & 15u : 8u) : c0;
                 s0[u] = scale(j + kU * kStep);
                 if (G == 32) s1[u] = scale(j + kU * kStep + 1);
                 uint32_t a[32];
@@ -329,25 +332,25 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         // ---- epilogue: accumulator -> Y ----
         const bool have = __all_sync(0xffffffffu, ok && wait_bounded(done, 0, abort_flag, err, kErrWaitDone, limit));
         tc_fence_after();
-        constexpr int HALF = BN / 2;                  // columns per warp of a lane quarter
-        constexpr int CH = 64;                        // and per round of loads
-        const int cbeg = h * HALF;
+        // The two warps of a lane quarter take 16 rows of the tile in turn.
+        constexpr int CH = 16;
         if (have) {
             // a whole tile goes through the (now idle) stage buffers, stored below by one TMA; every warp
             // store writes 64 contiguous bytes
             __nv_bfloat16 *ysm = (__nv_bfloat16 *)smem;
-            for (int c = cbeg; c < cbeg + HALF && c < unit.rows; c += CH) {
+            for (int c = h * CH; c < unit.rows; c += 2 * CH) {
                 float acc[CH];
 #pragma unroll
-                for (int u = 0; u < CH / 32; ++u) tmem_ld32(lane_addr + c + 32 * u, acc + 32 * u);
+                for (int u = 0; u < CH / 8; ++u) tmem_ld8(lane_addr + c + 8 * u, acc + 8 * u);
                 tmem_wait_ld();
                 if (tile_store) {
 #pragma unroll
                     for (int i = 0; i < CH; ++i) ysm[(c + i) * 128 + r] = __float2bfloat16_rn(acc[i]);
                 } else {
+                    __nv_bfloat16 *y = Y + (size_t)(m0 + c) * N + n;
 #pragma unroll
-                    for (int i = 0; i < CH; ++i)
-                        if (okn && c + i < unit.rows) Y[(size_t)(m0 + c + i) * N + n] = __float2bfloat16_rn(acc[i]);
+                    for (int i = 0; i < CH; ++i, y += N)
+                        if (okn && c + i < unit.rows) *y = __float2bfloat16_rn(acc[i]);
                 }
             }
         }
