@@ -27,10 +27,12 @@ __device__ __forceinline__ ExpertUnit find_unit(const ExpertPlan &p, int unit, i
 {
     const int lane = threadIdx.x & 31;
     ExpertUnit u = {0, 0, 0};
+    int next_lo = lane < p.E ? p.offsets[lane] : 0, next_hi = lane < p.E ? p.offsets[lane + 1] : 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        const int lo = e < p.E ? min(max(p.offsets[e], 0), p.P) : 0;
-        const int hi = e < p.E ? min(max(p.offsets[e + 1], 0), p.P) : 0;
+        const int lo = min(max(next_lo, 0), p.P), hi = min(max(next_hi, 0), p.P);
+        const int e = e0 + 32 + lane;                 // (asked for a round ahead)
+        next_lo = e < p.E ? p.offsets[e] : 0;
+        next_hi = e < p.E ? p.offsets[e + 1] : 0;
         const int n = max(hi - lo, 0), units = n / chunk + (n % chunk != 0);
         int upto = units;                             // units of the experts e0 .. e
 #pragma unroll
