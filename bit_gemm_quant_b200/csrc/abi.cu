@@ -293,11 +293,11 @@ w4_status w4_route(const void *logits, int logits_type, const float *bias, int64
 
 namespace {
 // Few rows an expert: the weight-streaming kernel, which dequantizes a weight
-// once per 8 rows; more: the tensor-core kernel, once per tile of 32 to 256.
-// Measured at 4 / 6 / 8 rows an expert on average, us: 8 experts [14336, 4096]
-// 82 / 97 / 128 against 105 / 113 / 120, 64 of [2048, 2048] 55 / 71 / 75 against
-// 71 / 71 / 72.
-bool experts_stream(int64_t P, int E) { return P <= 6 * (int64_t)E; }
+// once per 8 rows; more: the tensor-core kernel, once per tile of 128 or 256.
+// Measured at 4 / 5 / 6 rows an expert on average, us: 8 experts [14336, 4096]
+// 79 / 85 / 95 against 88 / 95 / 95, 64 of [2048, 2048] 52 / 56 / 68 against
+// 59 / 59 / 60, 128 of [768, 2048] 42 / 44 / 51 against 46 / 46 / 47.
+bool experts_stream(int64_t P, int E) { return P <= 5 * (int64_t)E; }
 }  // namespace
 
 size_t w4a16_experts_workspace_bytes(int64_t P, int E, int64_t K, int gathered)

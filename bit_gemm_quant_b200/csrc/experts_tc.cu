@@ -21,9 +21,11 @@
 // group size and mode are template parameters here, the loop is unrolled over the
 // ring, and a group's scale and zero-point word are loaded a round ahead and
 // looked at only where they are used.  8 of 8 experts [14336, 4096] with 8 rows
-// each: 105 us (37.6 of HBM).  With many rows, copies (576 clocks a k-block of 256
+// each: 101 us (37.6 of HBM), a chain of waits more than any one rate: 97 of 105
+// without the MMAs, 90 without the arithmetic, 82 without both; and 896 tiles
+// take four rounds of 296 CTAs.  With many rows, copies (576 clocks a k-block of 256
 // rows at 64 bytes a clock) and MMAs (512) alike: 8192 tokens, 2 of 8 experts:
-// 1647 us, 1168 TFLOP/s, 84% of the sustained cuBLAS rate (1828 with w4a16_gemm's
+// 1645 us, 1170 TFLOP/s, 84% of the sustained cuBLAS rate (1828 with w4a16_gemm's
 // loop by expert).
 #include "experts.cuh"
 #include "tc_pipe.cuh"
@@ -40,11 +42,6 @@ __device__ __noinline__ bool wait_pair_sleeping(uint64_t *a, uint64_t *b, uint32
            wait_bounded(b, parity, abort_flag, err, kErrWaitTma, limit);
 }
 
-// Shared memory: a ring of kStages boxes of X (a k-block each, as deep as the
-// ring of A stages in tensor memory) and one of kCodes boxes of codes (four
-// k-blocks each: 128 bytes of a row.  TMA spends two clocks on a row of 32 bytes
-// as on one of 128; with a box a k-block, as w4a16_gemm has, rows of codes were a
-// third to two thirds of the copies' time, and the copies what bounded the tile).
 __device__ __forceinline__ uint32_t elect_one()
 {
     uint32_t ok;
@@ -83,6 +80,12 @@ __device__ __forceinline__ bool mma_kblock_warp(uint32_t leader, uint32_t d_tmem
     return __all_sync(0xffffffffu, ok != 0);
 }
 
+// Shared memory: a ring of kStages boxes of X (a k-block each, as deep as the
+// ring of A stages in tensor memory) and one of kCodes boxes of codes (four
+// k-blocks each: 128 bytes of a row.  TMA spends two clocks on a row of 32 bytes
+// as on one of 128; with a box a k-block, as w4a16_gemm has, rows of codes were a
+// third to two thirds of the copies' time, and the copies what bounded the tile;
+// a third box of codes gains nothing).
 template <int BN>
 struct ExpTcCfg {
     using C = TcCfg<BN>;
@@ -443,9 +446,9 @@ cudaError_t launch_experts_tc(const void *X, ExpertPlan plan, int64_t N, int64_t
     // Rows of a tile by the rows an expert has on average: a larger tile shares a dequantized weight
     // among more rows, a smaller one has two CTAs on an SM.  (What an MMA computes past an expert's
     // last row is the same with both: at most 15 rows.)  Measured, us with 128 / 256: 8 experts
-    // [14336, 4096] at 32 rows each 108 / 148, 64: 113 / 152, 200: 220 / 213, 256: 265 / 257,
-    // 1024: 884 / 760; 64 of [2048, 2048] at 32: 71 / 97, 200: 151 / 158, 256: 186 / 181, 1024:
-    // 619 / 569; 128 of [768, 2048] at 200: 136 / 143, 300: 186 / 184.  (Tiles of 64 rows are within
+    // [14336, 4096] at 32 rows each 103 / 146, 64: 107 / 149, 200: 210 / 204, 256: 253 / 246,
+    // 1024: 853 / 738; 64 of [2048, 2048] at 32: 67 / 95, 200: 143 / 152, 256: 176 / 175, 1024:
+    // 596 / 556; 128 of [768, 2048] at 200: 129 / 137, 300: 179 / 179.  (Tiles of 64 rows are within
     // 2 % of 128's up to 12 rows an expert, on either side, and slower beyond.)
     const int64_t rows = plan.P / plan.E;
     const int BN = rows <= 224 ? 128 : 256;
