@@ -133,6 +133,20 @@ def test_uneven_plans(w4, T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("counts", [
+    (1, 15, 16, 17, 31, 33, 48, 64, 65, 100, 112, 113, 127, 128, 129, 0, 144, 257),
+    (255, 256, 257, 241, 240, 16, 1, 272, 600, 513),
+    (5, 5, 5, 5), (6, 6, 6, 6), (0, 0, 23, 1),
+], ids=["tiles_128", "tiles_256", "streaming", "few_rows", "few_rows_one_expert"])
+def test_rows_around_a_tile_and_an_mma(w4, counts):
+    """Experts whose last tile ends around the multiples of 16 that an MMA is
+    wide, around a tile, and averages on either side of the two kernels' limit."""
+    layer = Layer(w4, len(counts), 200, 320, 32, ASYM, seed=12)
+    ids = np.repeat(np.arange(len(counts), dtype=np.int32), counts)
+    check(w4, layer, np.random.default_rng(5).permutation(ids)[:, None], True)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("T", [3, 40, 400])
 def test_same_bits_again_and_on_another_stream(w4, T):
     import torch
