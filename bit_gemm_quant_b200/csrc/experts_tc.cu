@@ -143,11 +143,13 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     }
     if (warp == 1) tmem_alloc(tmem_slot, C::kCols);
     pdl_wait();                                                        // the plan is there
-    pdl_launch_dependents();
     const ExpertUnit unit = find_unit(plan, blockIdx.y, BN);           // (every warp finds the same)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // (not before this CTA has its tensor memory: a kernel started beside this one could take it, and waits
+    // for this one's end)
+    pdl_launch_dependents();
     const uint32_t tmem = *tmem_slot;
     if (unit.rows == 0) {                                              // fewer units than the grid has room for
         __syncthreads();
