@@ -587,7 +587,7 @@ cudaError_t launch_choose(const RouteArgs &a, bool fused, cudaStream_t stream)
     const size_t smem = a.groups > 1 ? (size_t)warps * (a.E + 64) * sizeof(uint64_t) : 0;
     static std::atomic<bool> attr_done[2][kMaxDevices];
     auto kern = fused ? route_fused_kernel<S, SIMPLE> : route_kernel<S, SIMPLE>;
-    if (smem > 48 * 1024) {
+    if (smem > 0) {                                       // (48 KB without the opt-in, static arrays included)
         const cudaError_t e = set_smem_attr(kern, (fused ? kFusedWarps : kRouteWarps) * (32 * S + 64) * 8, attr_done[fused]);
         if (e != cudaSuccess) return e;
     }
@@ -631,10 +631,8 @@ cudaError_t launch_route(const void *logits, int f32, const float *bias, int64_t
     }
     const int smem = (kPlanWarps + 2) * E * (int)sizeof(int);
     static std::atomic<bool> attr_done[kMaxDevices];
-    if (smem > 48 * 1024) {
-        const cudaError_t e2 = set_smem_attr(plan_many_kernel, (kPlanWarps + 2) * 1024 * (int)sizeof(int), attr_done);
-        if (e2 != cudaSuccess) return e2;
-    }
+    const cudaError_t e2 = set_smem_attr(plan_many_kernel, (kPlanWarps + 2) * 1024 * (int)sizeof(int), attr_done);
+    if (e2 != cudaSuccess) return e2;
     int id_bits = 0;
     while ((1 << id_bits) < E) ++id_bits;
     return launch_pdl(plan_many_kernel, dim3(kPlanCtas), dim3(kPlanWarps * 32), smem, stream, (const int *)ids, (int)P, E,

@@ -219,6 +219,32 @@ def test_choice_without_a_plan(w4):
     assert st == w4.W4_OK and torch.equal(ids, r.ids) and torch.equal(weights, r.weights)
 
 
+# Dynamic sizes just under 48 KB, where the kernels' static shared memory takes them over the limit without an
+# opt-in: route_fused_kernel has 1024 static bytes and T (E + 64) 8 dynamic ones with groups, plan_many_kernel 128
+# and 34 E 4.  In a process of its own: an earlier call with more memory would have opted the kernel in.
+BETWEEN = [dict(T=16, E=313 + 7, k=8, groups=8, keep=4), dict(T=15, E=344, k=8, groups=8, keep=4),
+           dict(T=14, E=368, k=8, groups=8, keep=4), dict(T=8, E=704, k=8, groups=8, keep=4),
+           dict(T=16, E=320, k=8, groups=8, keep=4, group_top=2, sigmoid=True),
+           dict(T=8, E=704, k=8, groups=8, keep=4, group_top=2, sigmoid=True),
+           dict(T=1030, E=361, k=32)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", BETWEEN, ids=lambda c: "T%d_E%d%s" % (c["T"], c["E"], "_fp64" if "sigmoid" in c else ""))
+def test_shared_memory_around_48_kb(case):
+    import json
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import json, sys; sys.path[:0] = [%r, %r]\n"
+            "import bit_gemm_quant_b200 as w4, test_parity_route as t\n"
+            "c = json.loads(sys.argv[1]); T, E, k = (c.pop(n) for n in ('T', 'E', 'k'))\n"
+            "t.check(w4, t.logits(T, E, 12), k, **c)\n" % (here, os.path.dirname(here)))
+    r = subprocess.run([sys.executable, "-c", code, json.dumps(case)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 # -------------------------------------------------------------- combine --
 
 @pytest.mark.gpu
