@@ -55,6 +55,7 @@ constexpr int kChunk = 8;                            // rows of a unit: the colu
 constexpr int kR = 2;                                // stages in flight per warp
 constexpr int kStageBytes = kRows * 128;
 constexpr int kRedBytes = kC * 32 * 16;              // one warp's partial tile
+__device__ const uint4 kZeros[4] = {};               // 32 activations behind the end of a row
 
 template <int G>
 struct ExpCfg {
@@ -327,12 +328,13 @@ experts_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *
 
         for (int st = j; st < NS && ok; st += KS) {
             // the activations of the stage, all in flight before anything waits: this lane's 32 elements of
-            // each half.  In a stage whose end lies behind K the codes and constants are 0 there, and the
-            // activations only have to be there.
+            // each half.  In a stage whose end lies behind K the codes and constants are 0 there; so are the
+            // activations, for an infinity among the row's own times 0 would be NaN.
             uint4 x[8];
 #pragma unroll
             for (int odd = 0; odd < 2; ++odd) {
-                const uint4 *p = (const uint4 *)(xrow + min(st * kSK + odd * 128 + 32 * t, K - 32));
+                const int k = st * kSK + odd * 128 + 32 * t;
+                const uint4 *p = k < K ? (const uint4 *)(xrow + k) : kZeros;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) x[4 * odd + w] = __ldg(p + w);
             }

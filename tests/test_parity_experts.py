@@ -274,6 +274,39 @@ def test_arrays_past_32_bits(w4, T):
     assert (Y[:, :-200] == 0).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 60], ids=["streaming", "tensor_core"])
+@pytest.mark.parametrize("K,g", [(320, 64), (32, 32), (96, 32), (544, 32), (640, 128), (512, 128)])
+def test_infinities_in_x(w4, K, g, T):
+    """An infinity in a row gives an infinity of the weight's sign, NaN where the weight is 0, in that row alone:
+    wherever it stands, the last columns of a K that is no whole stage among them."""
+    layer = Layer(w4, 3, 72, K, g, ASYM, seed=14)
+    ids = random_ids(T, 3, 1, 7)
+    offsets, order = plan_of(ids, 3)
+    assert (T <= 15) == (w4.w4a16_experts_workspace_bytes(T, 3, K, 1) == 0)      # the kernel that is meant
+    for cols in ((K - 1,), (K - 32,), (0,), (K // 2, K - 3)):
+        bits = synth.activations(21, T, K)
+        for i, c in enumerate(cols):
+            bits[i % T, c] = 0xFF80 if i else 0x7F80                             # +inf in row 0, -inf in row 1
+        x = synth.bf16_bits_to_f32(bits).astype(np.float64)
+        got = host_bf16_as_f64(layer(w4, dev_bf16(bits), torch_from(offsets), order=torch_from(order), top_k=1))
+        for i, row in enumerate(order):
+            e = ids[row, 0]
+            if np.isinf(x[row]).any():
+                c = int(np.argmax(np.isinf(x[row])))
+                with np.errstate(invalid="ignore"):
+                    want = x[row, c] * layer.w[e][:, c]
+                assert np.array_equal(got[i], want, equal_nan=True), (cols, row)
+            else:
+                assert_y_elementwise(got[i:i + 1], x[row:row + 1] @ layer.w[e].T,
+                                     np.abs(x[row:row + 1]) @ np.abs(layer.w[e]).T, K)
+
+
+def torch_from(a):
+    import torch
+    return torch.from_numpy(a).cuda()
+
+
 # ------------------------------------------------- the operators together --
 
 def forward(w4, x, r, gamma, gate, up, down, k, bias):
