@@ -127,6 +127,8 @@ __device__ __forceinline__ uint4 const_word(unsigned short s16bits, uint32_t zp)
     return make_uint4(c.shi, c.slo, c.z, 0u);
 }
 
+__device__ const uint4 kZeros[4] = {};        // 32 activations behind the end of a row
+
 template <int G, int MODE, int MT, int NW, int SK, int R, int MINB, bool EARLY, bool XPF>
 __global__ void __launch_bounds__(NW * 32, MINB)
 gemv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *__restrict__ X, int M, int N, int K,
@@ -233,16 +235,17 @@ gemv_kernel(const __grid_constant__ CUtensorMap tmap_q, const __nv_bfloat16 *__r
 
     // activations of chunk h of stage sb: 4 x 16 bytes per token group.  In a
     // stage that runs past the end of K (K is a multiple of 32, chunks are
-    // whole) a chunk past the end reads the last chunk's activations instead:
-    // its codes are zero-filled by TMA and its groups' constants have
-    // s16 = 0, so every w^ there is 0 and the activations only need to be finite
+    // whole) a chunk past the end reads zeros: its codes are zero-filled by TMA
+    // and its groups' constants have s16 = 0, so every w^ there is 0, and the
+    // row's own activations times 0 would be NaN where they are infinite
     auto load_x = [&](uint4 (&xv)[MT][4], int sb, int h) {
         const int kc = sb * SK + (h >> 1) * 256 + (h & 1) * 128;   // this lane adds t * 32
-        const int kk = (sb + 1) * SK <= K ? kc : min(kc + t * 32, K - 32) - t * 32;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int mt = 0; mt < MT; ++mt) {
+            const uint4 *p = kc + t * 32 < K ? (const uint4 *)(xrow[mt] + kc) : kZeros;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) xv[mt][w] = __ldg((const uint4 *)(xrow[mt] + kk) + w);
+            for (int w = 0; w < 4; ++w) xv[mt][w] = __ldg(p + w);
+        }
     };
 
     // two accumulator sets (the first and the second MMA of every word pair)

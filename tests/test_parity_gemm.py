@@ -231,3 +231,29 @@ def test_weights_static_flag_gives_the_same_bits(w4, M, N, K, g, mode):
     assert w4.w4_device_error() == 0
     if M * N <= 300000:
         check(ref, W, X, g, mode)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 2, 9, 16, 24])
+@pytest.mark.parametrize("K,g", [(320, 64), (32, 32), (96, 32), (544, 32), (640, 128), (4256, 32), (4096, 128)])
+def test_infinities_in_x(w4, K, g, M):
+    """An infinity in a row of X gives an infinity of the weight's sign, NaN where the weight is 0, in that row
+    alone, in either kernel and wherever it stands, the last columns of a K that is no whole stage among them."""
+    import torch
+    N = 72
+    q, s, z = w4.quant_pack(dev_bf16(synth.weights(31, N, K, 0.02)), g, ASYM)
+    eye = torch.zeros(4, K, dtype=torch.bfloat16, device="cuda")
+    cols = (K - 1, K - 32, 0, K // 2)
+    for i, c in enumerate(cols):
+        eye[i, c] = 1
+    w = host_bf16_as_f64(w4.gemm(eye, q, s, z, g, ASYM))                        # the columns of W^, exactly
+    for i, c in enumerate(cols):
+        bits = synth.activations(32, M, K)
+        plain = w4.gemm(dev_bf16(bits), q, s, z, g, ASYM)
+        bits[M // 2, c] = 0x7F80
+        got = w4.gemm(dev_bf16(bits), q, s, z, g, ASYM)
+        with np.errstate(invalid="ignore"):
+            want = np.inf * w[i]
+        assert np.array_equal(host_bf16_as_f64(got)[M // 2], want, equal_nan=True), c
+        others = [m for m in range(M) if m != M // 2]
+        assert torch.equal(got[others], plain[others])
