@@ -27,8 +27,8 @@ std::atomic<int> g_stall_first_wait{0};
 
 uint64_t wait_limit_ns()
 {
-    return g_wait_limit_ns.load(std::memory_order_relaxed) |
-           (g_stall_first_wait.load(std::memory_order_relaxed) ? kStallFirstWait : 0);
+    const int stall = g_stall_first_wait.load(std::memory_order_relaxed);
+    return g_wait_limit_ns.load(std::memory_order_relaxed) | (stall == 2 ? kStallLastMma : stall ? kStallFirstWait : 0);
 }
 
 bool gemm_shape_supported(int64_t M, int64_t N, int64_t K)
@@ -349,7 +349,7 @@ void w4_set_wait_limit_ns(uint64_t ns)
     w4::g_wait_limit_ns.store(ns > w4::kDefaultWaitNs ? w4::kDefaultWaitNs : ns, std::memory_order_relaxed);
 }
 
-void w4_test_stall_first_wait(int on) { w4::g_stall_first_wait.store(on ? 1 : 0, std::memory_order_relaxed); }
+void w4_test_stall_first_wait(int on) { w4::g_stall_first_wait.store(on, std::memory_order_relaxed); }
 
 w4_status w4_device_error(int *code)
 {

@@ -145,13 +145,15 @@ int read_and_clear_device_error();
 // w4_set_wait_limit_ns).  Waits that drain copies before a CTA exits always
 // keep the default.
 constexpr uint64_t kDefaultWaitNs = 200000000ull;   // 200 ms; no legitimate wait comes near it
-// The kernels receive the limit in the low 63 bits of a launch parameter; the
+// The kernels receive the limit in the low 62 bits of a launch parameter; the
 // top bit, set only by w4_test_stall_first_wait, makes each warp's first wait
-// for a copy target a barrier that nothing completes, so that it runs out.
-constexpr uint64_t kStallFirstWait = 1ull << 63;
+// for a copy target a barrier that nothing completes, so that it runs out, and
+// the next one the MMA issuer's last wait.
+constexpr uint64_t kStallFirstWait = 1ull << 63, kStallLastMma = 1ull << 62;
 uint64_t wait_limit_ns();
-__host__ __device__ inline uint64_t wait_limit_of(uint64_t w) { return w & ~kStallFirstWait; }
+__host__ __device__ inline uint64_t wait_limit_of(uint64_t w) { return w & ~(kStallFirstWait | kStallLastMma); }
 __host__ __device__ inline bool stalls_first_wait(uint64_t w) { return (w & kStallFirstWait) != 0; }
+__host__ __device__ inline bool stalls_last_mma(uint64_t w) { return (w & kStallLastMma) != 0; }
 // Device address of the library's error word on the current device (nullptr on failure).
 int *device_error_word();
 

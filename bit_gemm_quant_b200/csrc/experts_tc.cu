@@ -214,11 +214,12 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         const uint32_t fa0 = smem_u32(full_a), fb0 = smem_u32(full_b), em0 = smem_u32(empty);
         bool ready = false, stop = false;
         uint32_t ph = 0;
-        for (int i0 = 0; i0 < nkb && !stop; i0 += kStages, ph ^= 1u) {
+        const int nmma = stalls_last_mma(wait_ns) ? nkb - 1 : nkb;     // (failure-path tests only)
+        for (int i0 = 0; i0 < nmma && !stop; i0 += kStages, ph ^= 1u) {
 #pragma unroll
             for (int st = 0; st < kStages; ++st) {
                 const int i = i0 + st;
-                if (i >= nkb) break;
+                if (i >= nmma) break;
                 if (!ready)
                     ready = __all_sync(0xffffffffu,
                                        wait_pair_sleeping(&full_a[st], &full_b[st], ph, abort_flag, err, limit));
@@ -230,13 +231,16 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
                 // the next k-block's stage and phase (the last k-block re-tests its own, complete, barriers)
                 const int s1 = (st + 1 == kStages) ? 0 : st + 1;
                 const uint32_t ph1 = (st + 1 == kStages) ? (ph ^ 1u) : ph;
-                const bool last = i + 1 == nkb;
+                const bool last = i + 1 == nmma;
                 ready = mma_kblock_warp(leader, tmem_u, tmem_u + C::kACol0 + st * 32,
                                         bdesc0 + (uint64_t)((st * C::kBBytes) >> 4), idesc, i > 0 ? 1u : 0u,
                                         em0 + 8 * st, fa0 + 8 * (last ? st : s1), fb0 + 8 * (last ? st : s1),
                                         last ? ph : ph1);
             }
         }
+        if (nmma < nkb && !stop) stop = !wait_bounded(stall, 0, abort_flag, err, kErrWaitFullA, limit / 4);
+        if (stop) __threadfence_block();               // the abort flag is up before `done` completes
+        __syncwarp();
         if (leader) mma_commit(done);
         __syncwarp();
         wait_drain(done, 0, err);       // no MMA may still be running when tensor memory is freed
@@ -335,7 +339,9 @@ experts_tc_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         }
 
         // ---- epilogue: accumulator -> Y ----
-        const bool have = __all_sync(0xffffffffu, ok && wait_bounded(done, 0, abort_flag, err, kErrWaitDone, limit));
+        // (`done` also completes when the issuer gave up: the flag, raised before, tells)
+        const bool have = __all_sync(0xffffffffu, ok && wait_bounded(done, 0, abort_flag, err, kErrWaitDone, limit) &&
+                                                      *abort_flag == 0);
         tc_fence_after();
         // The two warps of a lane quarter take 16 rows of the tile in turn.
         constexpr int CH = 16;

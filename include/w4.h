@@ -575,7 +575,10 @@ void w4_set_wait_limit_ns(uint64_t ns);
  * w4a16_gemm and w4_mx_gemm) targets a barrier that nothing completes, so that it runs out
  * after the limit set by w4_set_wait_limit_ns and the kernel takes its failure
  * path; the copies it issued still land (they are drained with the default
- * limit).  0 (the default) turns it off.  Process-wide; read at each launch.
+ * limit).  The value 2 stalls another wait instead, the last one of
+ * w4a16_experts_gemm's MMA issuer, for a quarter of the limit: the sums are
+ * then incomplete although nothing else has failed.  0 (the default) turns it
+ * off.  Process-wide; read at each launch.
  */
 void w4_test_stall_first_wait(int on);
 

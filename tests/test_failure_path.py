@@ -106,3 +106,31 @@ def test_mx_product_wait_runs_out_then_next_call_is_correct(w4, M, N, K):
     assert w4.w4_device_error() == 0
     Y_ref, Y_abs = oracle_chain(X, W)[:2]
     assert_y_elementwise(Y, Y_ref, Y_abs, K, "Y after a failed call")
+
+
+@pytest.mark.gpu
+def test_a_late_failure_stores_no_partial_sums(w4):
+    """The products by expert: the MMA issuer's last wait runs out when every
+    other part of the pipeline has finished.  The sums lack a k-block; no tile,
+    whole or ragged, is stored, and the next call is correct."""
+    import torch
+    from test_parity_experts import Layer, check, plan_of
+    layer = Layer(w4, 3, 200, 320, 64, ASYM, seed=16)
+    ids = np.repeat(np.arange(3, dtype=np.int32), (128, 50, 300))[:, None]
+    offsets, order = (torch.from_numpy(a).cuda() for a in plan_of(ids, 3))
+    X = dev_bf16(synth.activations(17, len(ids), 320))
+    out = torch.full((len(ids), 200), 777.0, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    assert w4.w4_device_error() == 0
+    w4.w4_set_wait_limit_ns(20_000_000)           # 20 ms: the other waits are not short of time
+    w4.w4_test_stall_first_wait(2)
+    try:
+        layer(w4, X, offsets, order=order, top_k=1, out=out)
+        torch.cuda.synchronize()
+        code = w4.w4_device_error()
+    finally:
+        w4.w4_test_stall_first_wait(0)
+        w4.w4_set_wait_limit_ns(0)
+    assert code == 0x102, hex(code)
+    assert (out == 777).all()
+    check(w4, layer, ids, True)
