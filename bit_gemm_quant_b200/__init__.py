@@ -454,7 +454,8 @@ def _need(t, what: str, dtype, shape, device) -> None:
 def _elsewhere(helper, stream, first, *args):
     """helper(first, *args) with `first`'s device current and, where a stream is
     given, that stream: outputs and scratch are allocated on the stream that
-    writes them."""
+    writes them, and the memory of what was given is not handed out again before
+    that stream is done with it, even where the caller drops it at once."""
     import torch
     if not first.is_cuda:
         raise ValueError("%s: CUDA tensors are needed" % helper.__name__)
@@ -464,7 +465,12 @@ def _elsewhere(helper, stream, first, *args):
     if stream.device != first.device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, first.device))
     with torch.cuda.stream(stream):
-        return helper(first, *args)
+        result = helper(first, *args)
+    for a in (first, *args):
+        for t in a if isinstance(a, (tuple, list)) else (a,):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
+    return result
 
 
 def _run(name: str, index: int, *args) -> None:

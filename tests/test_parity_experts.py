@@ -307,6 +307,51 @@ def torch_from(a):
     return torch.from_numpy(a).cuda()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["rmsnorm", "rmsnorm_mxfp8", "route", "experts_gemm", "combine"])
+def test_inputs_dropped_behind_a_call_on_a_side_stream(w4, name):
+    """With stream= the inputs' memory is not handed out again before the kernel has read them, although the
+    caller drops them right behind the call."""
+    import torch
+    T, K, E, k, N = 64, 512, 8, 2, 136
+    layer = Layer(w4, E, N, K, 64, ASYM, seed=15)
+    ids = random_ids(T, E, k, 1)
+    n = lambda *shape: torch.randn(*shape, device="cuda")
+    offsets, order = (torch.from_numpy(a).cuda() for a in plan_of(ids, E))
+    pos = torch.argsort(order.long()).int().view(T, k)
+    x, r, gamma = n(T, K).bfloat16(), n(T, K).bfloat16(), n(K).bfloat16()
+    calls = {
+        "rmsnorm": (w4.rmsnorm, (x, gamma, 1e-6, r), {}),
+        "rmsnorm_mxfp8": (w4.rmsnorm_mxfp8, (x, gamma, 1e-6, r), {}),
+        "route": (w4.route, (n(T, E), k), dict(scoring=w4.SIGMOID, bias=n(E), n_groups=4, topk_groups=3, group_top=2)),
+        "experts_gemm": (w4.experts_gemm, (x, layer.q, layer.s, layer.z, 64, ASYM, offsets, order, k), {}),
+        "combine": (w4.combine, (n(T * k, N).bfloat16(), pos, n(T, k)), dict(add=n(T, N).bfloat16())),
+    }
+    fn, args, kw = calls[name]
+    want = [t.clone() for t in flat(fn(*args, **kw))]
+    side = torch.cuda.Stream()
+    fn(*args, **kw, stream=side)
+    zeros = lambda: [torch.empty_like(args[0]).zero_() for _ in range(64)]
+    zeros()                                              # (nothing below has to wait for memory or a kernel's code)
+    copy = lambda v: v.clone() if isinstance(v, torch.Tensor) else v
+    args2, kw2 = [copy(v) for v in args], {key: copy(v) for key, v in kw.items()}
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)                   # some 50 ms: the call below is still to come
+    got = fn(*args2, stream=side, **kw2)
+    del args2, kw2
+    fill = zeros()                                       # on the current stream, at once
+    torch.cuda.synchronize()
+    assert len(fill) == 64
+    for a, b in zip(flat(got), want):
+        assert torch.equal(a, b)
+
+
+def flat(v):
+    import torch
+    return [v] if isinstance(v, torch.Tensor) else [t for t in v if t is not None]
+
+
 # ------------------------------------------------- the operators together --
 
 def forward(w4, x, r, gamma, gate, up, down, k, bias):
