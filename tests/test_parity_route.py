@@ -245,6 +245,68 @@ def test_shared_memory_around_48_kb(case):
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+def pairs_of_choices(sigmoid, count, seed):
+    """(logits, scores' leading parts, what is left) of `count` fp32 logits whose exact score lies within 2^-30
+    of an fp32 value, so that the rest of it, score - fp32(score), is an fp32 value to 2^-54 of the score."""
+    # (a sigmoid above 16 is 1 to fp32)
+    x = np.random.default_rng(seed).uniform(-40, 16 if sigmoid else 0, 1 << 20).astype(np.float32)
+    e = np.exp(-np.abs(x.astype(np.longdouble)))         # 64 bits of mantissa
+    s = np.where(x < 0, e / (1 + e), 1 / (1 + e))         # softmax of (x, 0) is the sigmoid of x
+    lead = s.astype(np.float32)
+    rest = s - lead
+    near = np.flatnonzero(np.abs(rest) <= 2.0 ** -30 * s)[:count]
+    assert near.size == count and np.finfo(np.longdouble).nmant >= 63
+    return x[near], s[near], lead[near], rest[near]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_the_last_bits_of_the_scores(w4, sigmoid):
+    """Scores to their last bits, as the choice with a bias sees them.
+
+    Of each token two experts compete: one with the logit x and the bias -fp32(score), whose choice is what is
+    left of its score (the subtraction of near values is exact), and one with a score of 0 (logit -2000) and a
+    bias just below or above the exact rest.  Which is chosen tells the score to the distance between the two.
+
+    Distance, in u = 2^-53 of the score.  exp of v <= 0: its reduced argument is off by at most 0.7 u, the two
+    last steps of the polynomial by u (1 + 0.6), those before and the truncation by 0.3: 2.6.  Sigmoid: 1 + e
+    1 + 2.6 / 2, its reciprocal 1.1, and for x < 0 the exponential (whose own error then counts once in all) and
+    the product 1: below 6.  Softmax of x and 0: 2.6, the sum 1 + 1.3, its reciprocal 1, the product 1: below 7."""
+    u = 2.0 ** -53
+    tol = (6 if sigmoid else 7) * u
+    T = 511
+    x, s, lead, rest = pairs_of_choices(sigmoid, T, 3)
+    E = 2 * T + 1
+    logits = np.full((T, E), -np.inf, np.float32)
+    t = np.arange(T)
+    logits[t, 2 * t], logits[t, 2 * t + 1] = x, -2000.0
+    logits[:, E - 1] = 0.0                               # the softmax's other term, never chosen
+    for side in (-1, 1):
+        edge = rest + side * tol * s
+        other = edge.astype(np.float32)
+        wrong = (other - edge) * side < 0                # rounded towards the rest: one step outwards
+        other[wrong] = np.nextafter(other[wrong], np.float32(side * np.inf))
+        # the fp32 steps leave the edge close: no more than another 2^-53 away
+        assert (np.abs(other - edge) <= u * s).all()
+        bias = np.empty(E, np.float32)
+        bias[0:-1:2], bias[1:-1:2], bias[-1] = -lead, other, -4.0
+        got = w4.route(dev_f32(logits), 1, scoring=w4.SIGMOID if sigmoid else w4.SOFTMAX, bias=dev_f32(bias))
+        assert np.array_equal(got.ids.cpu().numpy()[:, 0], 2 * t + (side > 0)), "side %d" % side
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_near_scores_are_told_apart_with_a_bias(w4, sigmoid):
+    """Logits one fp32 step apart on the path that orders by fp64 scores."""
+    x = np.full((2, 64), 1.0, np.float32)
+    x[:, 40] = np.nextafter(np.float32(1), np.float32(2))
+    x[:, 50] = np.nextafter(x[:, 40], np.float32(2))
+    r = check(w4, x, 3, sigmoid=sigmoid, bias=np.full(64, 0.25, np.float32))
+    assert r.ids[0].tolist() == [50, 40, 0]
+    r = check(w4, x, 3, sigmoid=sigmoid, groups=8, keep=3, group_top=2)
+    assert r.ids[1].tolist() == [50, 40, 0]
+
+
 # -------------------------------------------------------------- combine --
 
 @pytest.mark.gpu
