@@ -352,6 +352,30 @@ def flat(v):
     return [v] if isinstance(v, torch.Tensor) else [t for t in v if t is not None]
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 64], ids=["streaming", "tensor_core"])
+def test_values_past_32_bits(w4, T):
+    """Each value of a product whose weights lie behind 2^32 bytes of codes, within one rounding of the exact sum;
+    other weights stand where an index cut to 32 bits would read."""
+    import torch
+    E, N, K, g, n = 9, 131072, 8192, 128, 200
+    q = torch.zeros(E, N, K // 8, dtype=torch.int32, device="cuda")
+    s = torch.zeros(E, N, K // g, dtype=torch.float16, device="cuda")
+    last = w4.quant_pack(dev_bf16(synth.weights(77, n, K, 0.02)), g, SYM)
+    decoy = w4.quant_pack(dev_bf16(synth.weights(78, n, K, 0.02)), g, SYM)
+    wrapped = (E * N * (K // 2) - 2 ** 32) // (K // 2)      # this row of codes lies 2^32 bytes in front of the end
+    q.view(E * N, -1)[wrapped - n:wrapped], s.view(E * N, -1)[wrapped - n:wrapped] = decoy[0], decoy[1]
+    q[-1, -n:], s[-1, -n:] = last[0], last[1]
+    bits = synth.activations(79, T, K)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[-1] = T
+    got = w4.experts_gemm(dev_bf16(bits), q, s, None, g, SYM, offsets)
+    w = dequantize(last[0].cpu().numpy().view(np.uint32)[None], last[1].cpu().numpy()[None], None, g)[0]
+    x = synth.bf16_bits_to_f32(bits).astype(np.float64)
+    assert_y_elementwise(host_bf16_as_f64(got[:, -n:]), x @ w.T, np.abs(x) @ np.abs(w).T, K)
+    assert (got[:, :-n] == 0).all()
+
+
 # ------------------------------------------------- the operators together --
 
 def forward(w4, x, r, gamma, gate, up, down, k, bias):
