@@ -36,7 +36,7 @@ struct NormArgs {
     __nv_bfloat16 *h, *y;
     uint8_t *codes, *scales;
     int64_t M;
-    int K, mma, sf_words;   // sf_words: scales leave in 32-bit words
+    int K, mma, sf_words, in_place;   // sf_words: scales leave in 32-bit words; in_place: an output over an input
     float eps;
 };
 
@@ -102,13 +102,19 @@ __global__ void __launch_bounds__(1024 / (VPT > 2 ? 2 : 1)) rmsnorm_vec_kernel(N
     const int o = SHIFT ? (int)((row * a.K) & 7) : 0;
     const int nv = SHIFT ? (o + a.K + 7) >> 3 : a.K >> 3;   // vectors of a row
     const int64_t v0 = (row * a.K) >> 3;                    // the first
-    const int64_t whole = SHIFT ? (a.M * a.K) >> 3 : 0;     // vectors that lie inside the arrays
+    // The vectors lo .. lo + whole - 1 are loaded as such: those inside the arrays, and, where an output lies over
+    // an input, inside the row (another CTA may be writing the other row's part of a shared one).
+    const int lo = SHIFT && a.in_place && o > 0;
+    const int whole = !SHIFT ? nv : a.in_place ? max(((o + a.K) >> 3) - lo, 0)
+                                               : (int)min(((a.M * a.K) >> 3) - v0, (int64_t)nv);
     auto load = [&](const __nv_bfloat16 *p, int v) {
-        if (v >= nv) return make_uint4(0u, 0u, 0u, 0u);
-        if (!SHIFT || v0 + v < whole) return ((const uint4 *)p)[v0 + v];
-        uint32_t w[4] = {0u, 0u, 0u, 0u};                   // the arrays end inside this vector
-        for (int64_t e = (v0 + v) * 8; e < a.M * a.K; ++e)
-            w[(e & 7) >> 1] |= (uint32_t)__bfloat16_as_ushort(p[e]) << (16 * (e & 1));
+        if ((unsigned)(v - lo) < (unsigned)whole) return ((const uint4 *)p)[v0 + v];
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (SHIFT && v < nv) {                              // this row's elements alone
+            const int k = 8 * v - o;
+            for (int64_t e = row * a.K + max(k, 0); e < row * a.K + min(k + 8, a.K); ++e)
+                w[(e & 7) >> 1] |= (uint32_t)__bfloat16_as_ushort(p[e]) << (16 * (e & 1));
+        }
         return make_uint4(w[0], w[1], w[2], w[3]);
     };
     auto store = [&](__nv_bfloat16 *p, int v, const float (&f)[8]) {
@@ -257,7 +263,7 @@ cudaError_t launch_rmsnorm(const void *X, const void *residual, const void *gamm
     const int mma = codes && layout == W4_MX_SCALES_MMA;
     NormArgs a = {(const __nv_bfloat16 *)X, (const __nv_bfloat16 *)residual, (const __nv_bfloat16 *)gamma,
                   (__nv_bfloat16 *)H, (__nv_bfloat16 *)Y, codes, scales, M, (int)K,
-                  mma, K % 128 == 0 && (uintptr_t)scales % 4 == 0, eps};
+                  mma, K % 128 == 0 && (uintptr_t)scales % 4 == 0, Y == X || (H && (H == X || H == residual)), eps};
     const uintptr_t all = (uintptr_t)X | (uintptr_t)residual | (uintptr_t)gamma | (uintptr_t)H | (uintptr_t)Y;
     if (all % 16 != 0) {
         const int threads = K >= 1024 ? 1024 : (int)((K + 31) / 32 * 32);

@@ -169,6 +169,23 @@ def test_in_place(w4, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("M,K", [(9000, 7), (5000, 129), (3000, 1003), (700, 4098), (333, 32767), (2, 1001)])
+def test_in_place_rows_that_share_vectors(w4, M, K):
+    """Rows that are no whole vectors, in place: many at once on either side of every shared vector, and the
+    arrays' own end."""
+    import torch
+    x, r, gamma = (dev(a) for a in inputs(M, K, 22))
+    Y, H = w4.rmsnorm(x, gamma, EPS, residual=r)
+    for _ in range(3):
+        x1, r1 = x.clone(), r.clone()
+        w4.rmsnorm(x1, gamma, EPS, residual=r1, out=(x1, r1))
+        assert torch.equal(x1, Y) and torch.equal(r1, H)
+    x2, Y2 = x.clone(), torch.empty_like(x)
+    w4.rmsnorm(x2, gamma, EPS, residual=r, out=(Y2, x2))
+    assert torch.equal(Y2, Y) and torch.equal(x2, H)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("K", [256, 1024, 1003])
 def test_zero_rows_and_extremes(w4, K):
     """An all-zero row gives zeros; x = -r gives zeros; tiny rows stand on eps;
