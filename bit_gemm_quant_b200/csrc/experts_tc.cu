@@ -13,7 +13,8 @@
 // (x, y) owns the channels 128 x .. of one expert and up to BN of that expert's
 // rows (unit y of the plan); N and the channels are per expert.  A box's rows
 // past the unit's are other rows of X: the MMAs leave them out from the next
-// multiple of 16 on, and their accumulator columns are never stored; a whole tile of rows leaves by TMA, a ragged one by plain stores.
+// multiple of 16 on, and their accumulator columns are never stored; a whole tile
+// of rows leaves by TMA, a ragged one by plain stores.
 //
 // What bounds it.  With few rows an expert, the dequantization: 157 instructions
 // per warp and k-block (2.4 a weight), whatever BN is, in whose way the MMA
@@ -25,8 +26,8 @@
 // without the MMAs, 90 without the arithmetic, 82 without both; and 896 tiles
 // take four rounds of 296 CTAs.  With many rows, copies (576 clocks a k-block of 256
 // rows at 64 bytes a clock) and MMAs (512) alike: 8192 tokens, 2 of 8 experts:
-// 1645 us, 1170 TFLOP/s, 84% of the sustained cuBLAS rate (1828 with w4a16_gemm's
-// loop by expert).
+// 1645 to 1710 us on several B200s, 1125 to 1170 TFLOP/s, 81 to 84% of the sustained
+// cuBLAS rate (1828 with w4a16_gemm's loop by expert).
 #include "experts.cuh"
 #include "tc_pipe.cuh"
 

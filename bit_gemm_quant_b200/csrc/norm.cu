@@ -17,9 +17,11 @@
 // within a thread, then a butterfly over the warp, then over the CTA's warps
 // through shared memory, always in the same order.
 //
-// What bounds it: HBM.  8192 rows of 8192, residual, MXFP8 out (472 MB): 77 us,
-// 6.1 TB/s, 93% of the measured copy rate; with x and r loaded one after the
-// other 110.  One row of 4096: 1.8 us in a graph, launch and latency.
+// What bounds it: HBM.  8192 rows of 8192, residual: MXFP8 out (472 MB) 77 to 81
+// us on two B200s, 5.8 to 6.1 TB/s, 89 to 93% of the measured copy rate (with x
+// and r loaded one after the other 110); bf16 out (537 MB) 82 us, the copy rate.
+// 8192 rows of 5003, residual, bf16 out (328 MB): 62 us, 81%; gamma comes in single
+// elements there.  One row of 4096: 1.9 us in a graph, launch and latency.
 //
 // Rounding: everything between the bf16 inputs and the outputs is fp32.  h is
 // rounded to bf16 for H alone; the norm uses the fp32 sum, and the codes are

@@ -27,10 +27,10 @@
 // pairs in order; more pairs are counted and placed by one cluster.  Up to
 // kFusedPairs pairs of kFusedWarps tokens the one CTA that chooses also makes the
 // plan, each thread ranking one pair against all others in shared memory: one
-// launch in place of two.  (57 tokens that way took 11.9 us, against 5.2 in two.)
+// launch in place of two.  (57 tokens that way took 11.9 us, against 4.3 in two.)
 // What bounds it: latency.  8192 tokens, 8 of 128 experts (4.7 MB, 0.8 us of HBM)
-// take 18 us, 8.5 of them the choice; one token, 8 of 256 experts in 8 groups,
-// sigmoid and bias, 7.8 us, half of it the fp64 scores.
+// take 17.4 us, 8.7 of them the choice; 8 of 256 in 8 groups by sigmoid and bias 34;
+// one token so, 8.3 us, half of it the fp64 scores.
 #include "common.cuh"
 
 #include <cooperative_groups.h>
@@ -515,7 +515,8 @@ plan_many_kernel(const int *ids, int P, int E, int id_bits, int *offsets, int *o
 // One thread sums 8 (VEC) or 1 columns of one token, the rows of up to kAhead
 // pairs in flight at once; `parts` CTAs share a token's columns.  The sum runs in
 // fp32 in the order of the pairs.  What bounds it: HBM, each row of Y read once
-// (8192 tokens, 8 experts, N = 4096, with a shared expert: 672 MB, 102 us).
+// (8192 tokens, 8 experts, N = 4096, with a shared expert: 672 MB in 110 to 112 us
+// on two B200s, 92 to 94% of the copy rate).
 constexpr int kAhead = 8;
 
 template <bool VEC>
@@ -623,8 +624,14 @@ cudaError_t launch_route(const void *logits, int f32, const float *bias, int64_t
     const bool simple = !bias && (groups == 1 || group_top == 1);
     const cudaError_t e = simple ? launch_experts<true>(a, fused, stream) : launch_experts<false>(a, fused, stream);
     if (e != cudaSuccess || !offsets || fused) return e;
-    // Both kernels for the plan after a choice, us: 4096 pairs of 128 experts 3.1 (a CTA for each expert)
-    // and 7.4 (a cluster), 65536 pairs 12 and 9.5.
+    // Both kernels for the plan behind the choice, us, a CTA for each expert / a cluster:
+    //   pairs      4096        16384       32768       65536
+    //   32 experts  3.6 / 6.3   4.6 / 6.5   6.7 / 6.8  12.8 / 7.7
+    //   128         3.6 / 7.0   6.7 / 7.6   8.6 / 7.9  18.2 / 8.8
+    //   256         3.7 / 7.6  10.4 / 7.9   9.9 / 6.3  18.3 / 9.2
+    //   1024        5.2 / 9.7  20.6 / 10   27.4 / 11   56.4 / 11
+    // The rule goes by the pairs alone: with many experts the cluster would be ahead from fewer pairs on
+    // (256: about 12000, 1024: about 6000).
     if (P <= kPlanMany) {
         const int threads = P >= 8192 ? 1024 : 256;
         return launch_pdl(plan_kernel, dim3(E), dim3(threads), 0, stream, (const int *)ids, (int)P, E, offsets, order, pos);
