@@ -347,6 +347,34 @@ def test_inputs_dropped_behind_a_call_on_a_side_stream(w4, name):
         assert torch.equal(a, b)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 90])
+def test_a_given_stream_under_capture(w4, T):
+    """stream= naming the capturing stream, inputs dropped behind the calls that read them."""
+    import torch
+    layer = Layer(w4, 8, 136, 512, 64, ASYM, seed=17)
+    x, r, gamma, gate, bias = layer_inputs(w4, T, 512, 0, 8, 5)
+    side = torch.cuda.Stream()
+
+    def run(stream):
+        y, h = w4.rmsnorm(x, gamma, 1e-6, residual=r, stream=stream)
+        plan = w4.route(y.float() @ gate, 2, scoring=w4.SIGMOID, bias=bias, stream=stream)
+        a = layer(w4, y, plan.offsets, order=plan.order, top_k=2, stream=stream)
+        return w4.combine(a, plan.pos, plan.weights, stream=stream), h
+
+    want = run(None)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        got = run(side)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    assert w4.w4_device_error() == 0
+
+
 def flat(v):
     import torch
     return [v] if isinstance(v, torch.Tensor) else [t for t in v if t is not None]
